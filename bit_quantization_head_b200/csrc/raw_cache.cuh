@@ -1,0 +1,95 @@
+// Shared by the calls around the cache and on the uncompressed pages: argument checks, the
+// current device's SM count and launches with programmatic stream serialization.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <utility>
+
+#include "kvtc_internal.h"
+
+namespace kvtc {
+namespace raw {
+
+constexpr int kRowElems = kD;                              // elements of one K or V row
+constexpr long long kKindElems = static_cast<long long>(kPage) * kD;  // K or V of one page and head
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Whether two buffers of the same size share memory.
+inline bool overlap(const void* a, const void* b, uint64_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bytes && y < x + bytes;
+}
+
+// The sizes and pointers every call on the uncompressed pages needs.
+inline kvtc_status check_cache(const kvtc_raw_cache* c, int layer) {
+  if (!c || !c->pool) return fail(KVTC_EINVAL, "cache is incomplete");
+  if (c->dtype != KVTC_BF16 && c->dtype != KVTC_F16) return fail(KVTC_EINVAL, "the pages' dtype must be BF16 or F16");
+  if (c->n_layers < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 1024 || c->n_pages < 1)
+    return fail(KVTC_EINVAL, "bad cache sizes");
+  // rows of all layers are counted in 31 bits (tensor map coordinates, page ids); the row
+  // count is bounded step by step, so no product overflows
+  const uint64_t row_limit = 1ull << 31;
+  const uint64_t per_page = 2ull * kPage * static_cast<uint64_t>(c->n_kv_heads);
+  if (c->n_pages >= row_limit / per_page || static_cast<uint64_t>(c->n_layers) > row_limit / (per_page * c->n_pages))
+    return fail(KVTC_EINVAL, "the pool has more than 2^31 rows");
+  if (layer < 0 || layer >= c->n_layers) return fail(KVTC_EINVAL, "layer out of range");
+  if (reinterpret_cast<uintptr_t>(c->pool) & 127) return fail(KVTC_EINVAL, "pool must be 128-byte aligned");
+  return KVTC_OK;
+}
+
+// What both attention calls need beyond that.
+inline kvtc_status check_attention(const kvtc_raw_cache* c, int layer, int n_q_heads, int max_group, int max_seq_len,
+                                   float scale) {
+  kvtc_status st = check_cache(c, layer);
+  if (st != KVTC_OK) return st;
+  if (!c->block_table) return fail(KVTC_EINVAL, "cache is incomplete");
+  if (c->n_seq < 1 || c->max_pages < 1 || c->max_pages >= (1 << 24)) return fail(KVTC_EINVAL, "bad sizes");
+  if (n_q_heads < 1 || n_q_heads % c->n_kv_heads != 0)
+    return fail(KVTC_EINVAL, "n_q_heads must be a positive multiple of n_kv_heads");
+  if (n_q_heads / c->n_kv_heads > max_group) return fail(KVTC_EINVAL, "too many query heads per KV head");
+  if (max_seq_len < 0 || max_seq_len > static_cast<long long>(c->max_pages) * kPage)
+    return fail(KVTC_EINVAL, "max_seq_len exceeds the block table");
+  if (!std::isfinite(scale) || scale < 0.0f) return fail(KVTC_EINVAL, "softmax_scale must be finite and >= 0");
+  return KVTC_OK;
+}
+
+// SM count of the current device (a constant of the device, read once for each).
+inline kvtc_status sm_count(int* out) {
+  static int known[64] = {};
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev >= 0 && dev < 64 && known[dev] > 0) {
+    *out = known[dev];
+    return KVTC_OK;
+  }
+  int n = 0;
+  e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess || n < 1) return cuda_fail(e, "device query");
+  if (dev >= 0 && dev < 64) known[dev] = n;
+  *out = n;
+  return KVTC_OK;
+}
+
+// Launch that may start while the previous kernel of the stream finishes; the kernel calls
+// griddepcontrol.wait before it touches memory.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch(void (*fn)(KArgs...), dim3 grid, int block, size_t smem, void* stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, fn, std::forward<Args>(args)...);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace raw
+}  // namespace kvtc

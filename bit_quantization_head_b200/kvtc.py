@@ -18,12 +18,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvtc.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "kvtc.h")
 
-KVTC_F32, KVTC_BF16 = 0, 1
+KVTC_F32, KVTC_BF16, KVTC_F16 = 0, 1, 2
 KIND_K, KIND_V = 0, 1
 WEIGHTS_KL, WEIGHTS_MSE = 0, 1
 C2_LAGRANGE, C2_DAMPED = 0, 1
 RAW_BITS = 16  # b of an uncompressed value unit (keys-only plans)
-STATUS_BAD_PAGE, STATUS_BAD_POS, STATUS_TIMEOUT = 1, 2, 4
+STATUS_BAD_PAGE, STATUS_BAD_POS, STATUS_TIMEOUT, STATUS_NO_PAGE = 1, 2, 4, 8
 PAGE_TOKENS = 128
 HEAD_DIM = 128
 STATUS_NAMES = {0: "OK", 1: "EINVAL", 2: "ENOMEM", 3: "ECUDA", 4: "EINFEASIBLE", 5: "ECAPACITY",
@@ -52,6 +52,16 @@ class UnitInfo(C.Structure):
 class CacheDesc(C.Structure):
     _fields_ = [("pool", C.c_void_p), ("pages_per_unit", C.c_uint64), ("block_table", C.c_void_p),
                 ("n_seq", C.c_int), ("max_pages", C.c_int), ("status", C.c_void_p)]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("n_axes", C.c_int), ("section", C.c_int * 4), ("interleaved", C.c_int), ("base", C.c_double)]
+
+
+class RawCacheDesc(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("n_layers", C.c_int), ("n_pages", C.c_uint64), ("n_kv_heads", C.c_int),
+                ("dtype", C.c_int), ("block_table", C.c_void_p), ("n_seq", C.c_int), ("max_pages", C.c_int),
+                ("status", C.c_void_p)]
 
 
 _lib = None
@@ -95,6 +105,19 @@ def lib():
                                                C.c_float, _P, C.c_int, _P]),
         "kvtc_decode_attention_rope": (st, [_P, C.POINTER(CacheDesc), C.c_int, _P, C.c_int, _P, C.c_int, C.c_float,
                                             C.c_double, _P, C.c_int, _P, C.c_uint64, _P]),
+        "kvtc_step_tables": (st, [_P, _P, C.c_int, _P, C.c_int, _P, _P, C.c_int, _P, _P, _P, _P, C.c_int, _P, _P,
+                                  _P, _P]),
+        "kvtc_rope": (st, [C.POINTER(RopeDesc), _P, C.c_int64, C.c_int, _P, C.c_int64, C.c_int, C.c_int, _P, C.c_int,
+                           C.c_int, _P, _P, _P]),
+        "kvtc_raw_cache_bytes": (C.c_uint64, [C.c_int, C.c_uint64, C.c_int]),
+        "kvtc_raw_append": (st, [C.POINTER(RawCacheDesc), C.c_int, _P, C.c_int64, _P, C.c_int64, _P, C.c_int,
+                                 C.POINTER(RopeDesc), _P, _P, C.c_int64, C.c_int, _P, _P]),
+        "kvtc_raw_decode_workspace_bytes": (C.c_uint64, [C.c_int] * 4),
+        "kvtc_raw_cross_workspace_bytes": (C.c_uint64, [C.c_int] * 5),
+        "kvtc_raw_decode_attention": (st, [C.POINTER(RawCacheDesc), C.c_int, _P, C.c_int, _P, C.c_int, C.c_float, _P,
+                                           _P, C.c_uint64, _P]),
+        "kvtc_raw_cross_attention": (st, [C.POINTER(RawCacheDesc), C.c_int, _P, C.c_int, _P, C.c_int, _P, C.c_int,
+                                          C.c_float, _P, _P, C.c_uint64, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -322,3 +345,180 @@ def kvtc_decode_attention_rope(plan, cache, layer, q, seq_lens, max_seq_len, out
                                             _dev_ptr(seq_lens), max_seq_len, scale, float(rope_base), _dev_ptr(out),
                                             _dtype_code(out), _dev_ptr(workspace),
                                             workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- serving step
+_I32, _I64 = "torch.int32", "torch.int64"
+_RAW_DTYPES = {"torch.float32": KVTC_F32, "torch.bfloat16": KVTC_BF16, "torch.float16": KVTC_F16}
+
+
+def _buf(t, dtype, name, shape=None):
+    """Device pointer of a contiguous tensor on the current device, of one dtype (and shape)."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if str(t.dtype) != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, name, n_tok=None):
+    """(pointer, token stride, heads) of rows [n_tok][heads][128] whose heads and elements
+    are dense (a slice of a fused projection passes as it is)."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if str(t.dtype) != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM or (n_tok is not None and t.shape[0] != n_tok):
+        raise ValueError(f"{name} must have shape [n_tok][heads][{HEAD_DIM}], got {tuple(t.shape)}")
+    n, heads, _ = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM):
+        raise ValueError(f"{name}: heads and elements must be dense")
+    return t.data_ptr(), (t.stride(0) if n > 1 else max(heads * HEAD_DIM, 1)), heads
+
+
+def kvtc_step_tables(cached_lens, new_lens, page_ring, ring_state, block_table, seq_lens, cu_seqlens, slot_map,
+                     positions, ring_state_out, workspace, status=None, stream=None):
+    """Tables of one serving step from the request lengths (all device tensors; int32, the
+    slot map int64).  ring_state_out may be ring_state and seq_lens may be cached_lens."""
+    n_seq, rows = cached_lens.numel(), slot_map.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape [n_seq][max_pages]")
+    max_pages = block_table.shape[1]
+    if workspace.numel() * workspace.element_size() < 16:
+        raise ValueError("workspace must hold 16 bytes")
+    _check(lib().kvtc_step_tables(
+        _buf(cached_lens, _I32, "cached_lens"), _buf(new_lens, _I32, "new_lens", (n_seq,)), n_seq,
+        _buf(page_ring, _I32, "page_ring"), page_ring.numel(), _buf(ring_state, _I32, "ring_state", (2,)),
+        _buf(block_table, _I32, "block_table", (n_seq, max_pages)), max_pages,
+        _buf(seq_lens, _I32, "seq_lens", (n_seq,)), _buf(cu_seqlens, _I32, "cu_seqlens", (n_seq + 1,)),
+        _buf(slot_map, _I64, "slot_map"), _buf(positions, _I32, "positions", (rows,)), rows,
+        _buf(ring_state_out, _I32, "ring_state_out", (2,)), _buf(workspace, str(workspace.dtype), "workspace"),
+        None if status is None else _buf(status, _I32, "status"), _stream(stream)))
+
+
+def rope_desc(sections, interleaved=False, base=0.0):
+    """Rotary description: pairs of each position axis (they sum to 64), consecutive or
+    interleaved, and the base (0 means 500000)."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 4:
+        raise ValueError("one to four axes")
+    return RopeDesc(len(sections), (C.c_int * 4)(*sections), 1 if interleaved else 0, float(base))
+
+
+def kvtc_rope(rope, q, k, positions, q_out, k_out, inverse=False, stream=None):
+    """Rotates q and/or k rows [n_tok][heads][128] to positions int32 [n_axes][n_tok]
+    (or [n_tok] for one axis); inverse: the transpose.  q or k may be None."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    dtype, n_tok = str(ref.dtype), ref.shape[0]
+    if dtype not in _RAW_DTYPES:
+        raise TypeError(f"unsupported dtype {ref.dtype}")
+    qp = _rows(q, dtype, "q", n_tok) if q is not None else (None, 0, 0)
+    kp = _rows(k, dtype, "k", n_tok) if k is not None else (None, 0, 0)
+    _check(lib().kvtc_rope(
+        C.byref(rope), *qp, *kp, _RAW_DTYPES[dtype], _positions_ptr(rope, positions, n_tok), n_tok,
+        1 if inverse else 0, None if q is None else _buf(q_out, dtype, "q_out", tuple(q.shape)),
+        None if k is None else _buf(k_out, dtype, "k_out", tuple(k.shape)), _stream(stream)))
+
+
+def _positions_ptr(rope, positions, n_tok):
+    if positions.numel() != rope.n_axes * n_tok or positions.shape[-1] != n_tok:
+        raise ValueError(f"positions must have shape [{rope.n_axes}][{n_tok}]")
+    return _buf(positions, _I32, "positions")
+
+
+# ---------------------------------------------------------------- uncompressed pages
+def kvtc_raw_cache_bytes(n_layers, n_pages, n_kv_heads):
+    return int(lib().kvtc_raw_cache_bytes(n_layers, n_pages, n_kv_heads))
+
+
+class RawCache:
+    """Uncompressed page cache: pool [n_layers][n_pages][n_kv_heads][K, V][128][128] (bf16 or
+    fp16), block table and status word (torch CUDA tensors), described to the library as a
+    kvtc_raw_cache.  An int32 block table on the device is used in place, so tables that
+    kvtc_step_tables grows are seen by later calls."""
+
+    def __init__(self, n_layers, n_kv_heads, n_pages, block_table, dtype=None, device="cuda", pool=None):
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"unsupported dtype {dtype}")
+        shape = (int(n_layers), int(n_pages), int(n_kv_heads), 2, PAGE_TOKENS, HEAD_DIM)
+        if pool is None:
+            pool = torch.zeros(shape, dtype=dtype, device=device)
+        if pool.dtype != dtype or tuple(pool.shape) != shape or not pool.is_contiguous() or not pool.is_cuda:
+            raise ValueError(f"pool must be a contiguous CUDA tensor {shape} of {dtype}")
+        self.pool = pool
+        self.block_table = block_table.to(device=pool.device, dtype=torch.int32).contiguous()
+        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self.dtype = str(dtype)
+        self.n_kv_heads = shape[2]
+        self.desc = RawCacheDesc(pool.data_ptr(), shape[0], shape[1], shape[2], _RAW_DTYPES[self.dtype],
+                                 self.block_table.data_ptr(), self.block_table.shape[0], self.block_table.shape[1],
+                                 self.status.data_ptr())
+
+    def _on_current_device(self):
+        import torch
+        if self.pool.device.index != torch.cuda.current_device():
+            raise ValueError("the cache must be on the current CUDA device")
+        return C.byref(self.desc)
+
+
+def kvtc_raw_append(cache, layer, k, v, slot_map, rope=None, positions=None, q=None, q_out=None, stream=None):
+    """Writes k, v rows [n_tok][n_kv_heads][128] into their slots (int64 [n_tok]) of one
+    layer's pages; with rope, k is rotated on the way, and q into q_out."""
+    n_tok, dtype = k.shape[0], cache.dtype
+    kp, vp = _rows(k, dtype, "k", n_tok), _rows(v, dtype, "v", n_tok)
+    if kp[2] != cache.n_kv_heads or vp[2] != cache.n_kv_heads:
+        raise ValueError(f"k and v must have {cache.n_kv_heads} heads")
+    if rope is not None and positions is None:
+        raise ValueError("rope needs positions")
+    qp = _rows(q, dtype, "q", n_tok) if q is not None else (None, 0, 0)
+    _check(lib().kvtc_raw_append(
+        cache._on_current_device(), layer, kp[0], kp[1], vp[0], vp[1], _buf(slot_map, _I64, "slot_map", (n_tok,)), n_tok,
+        None if rope is None else C.byref(rope), None if rope is None else _positions_ptr(rope, positions, n_tok),
+        *qp, None if q is None else _buf(q_out, dtype, "q_out", tuple(q.shape)), _stream(stream)))
+
+
+def kvtc_raw_decode_workspace_bytes(n_seq, n_q_heads, n_kv_heads, max_seq_len):
+    return int(lib().kvtc_raw_decode_workspace_bytes(n_seq, n_q_heads, n_kv_heads, max_seq_len))
+
+
+def kvtc_raw_cross_workspace_bytes(n_seq, n_tok, n_q_heads, n_kv_heads, max_seq_len):
+    return int(lib().kvtc_raw_cross_workspace_bytes(n_seq, n_tok, n_q_heads, n_kv_heads, max_seq_len))
+
+
+def _head_rows(cache, t, name, rows):
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must have shape [{rows}][n_q_heads][{HEAD_DIM}], got {tuple(t.shape)}")
+    return _buf(t, cache.dtype, name)
+
+
+def kvtc_raw_decode_attention(cache, layer, q, seq_lens, max_seq_len, out, workspace, scale=0.0, stream=None):
+    """One new token per sequence over one layer's uncompressed pages; q, out
+    [n_seq][n_q_heads][128] of the cache's dtype."""
+    n_seq = cache.desc.n_seq
+    qp = _head_rows(cache, q, "q", n_seq)
+    _check(lib().kvtc_raw_decode_attention(
+        cache._on_current_device(), layer, qp, q.shape[1], _buf(seq_lens, _I32, "seq_lens", (n_seq,)), max_seq_len,
+        scale, _buf(out, cache.dtype, "out", tuple(q.shape)), _buf(workspace, str(workspace.dtype), "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def kvtc_raw_cross_attention(cache, layer, q, cu_q, seq_lens, max_seq_len, out, workspace, scale=0.0, stream=None):
+    """Rows cu_q[s]..cu_q[s+1]-1 of q [n_tok][n_q_heads][128] attend to the first seq_lens[s]
+    tokens of sequence s's uncompressed pages (no causal mask)."""
+    n_seq = cache.desc.n_seq
+    qp = _head_rows(cache, q, "q", q.shape[0])
+    _check(lib().kvtc_raw_cross_attention(
+        cache._on_current_device(), layer, qp, q.shape[1], _buf(cu_q, _I32, "cu_q", (n_seq + 1,)), q.shape[0],
+        _buf(seq_lens, _I32, "seq_lens", (n_seq,)), max_seq_len, scale, _buf(out, cache.dtype, "out", tuple(q.shape)),
+        _buf(workspace, str(workspace.dtype), "workspace"), workspace.numel() * workspace.element_size(),
+        _stream(stream)))

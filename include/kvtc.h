@@ -54,7 +54,9 @@ typedef enum {
   KVTC_ESTATE = 8        /* plan not uploaded to the device (kvtc_plan_upload)         */
 } kvtc_status;
 
-typedef enum { KVTC_F32 = 0, KVTC_BF16 = 1 } kvtc_dtype;
+/* KVTC_F16 is a type of the calls around the cache (kvtc_rope and the uncompressed pages);
+ * the coded cache's calls take F32 and BF16. */
+typedef enum { KVTC_F32 = 0, KVTC_BF16 = 1, KVTC_F16 = 2 } kvtc_dtype;
 typedef enum { KVTC_KIND_K = 0, KVTC_KIND_V = 1 } kvtc_kind;
 typedef enum { KVTC_WEIGHTS_KL = 0, KVTC_WEIGHTS_MSE = 1 } kvtc_weight_mode;
 /* C2 solver: the Lagrangian water-filling (mu bisected, exact on the convex hull), or the
@@ -76,6 +78,7 @@ typedef enum { KVTC_C2_LAGRANGE = 0, KVTC_C2_DAMPED = 1 } kvtc_c2_mode;
 #define KVTC_STATUS_BAD_PAGE 1u      /* block table entry outside [0, pages_per_unit)  */
 #define KVTC_STATUS_BAD_POS 2u       /* position or length beyond max_pages * 128      */
 #define KVTC_STATUS_TIMEOUT 4u       /* a bounded wait on an mbarrier gave up          */
+#define KVTC_STATUS_NO_PAGE 8u       /* too few free pages for a sequence's new tokens */
 
 /* Thread-local description of the last error on this thread ("" if none). */
 const char* kvtc_last_error(void);
@@ -366,6 +369,164 @@ kvtc_status kvtc_decode_attention_noalloc(const kvtc_plan* plan, const kvtc_cach
                                           const void* q, kvtc_dtype q_dtype, const int32_t* seq_lens,
                                           int max_seq_len, float softmax_scale, void* out,
                                           kvtc_dtype out_dtype, void* stream);
+
+/* ------------------------------------------------------------------ serving step -- */
+
+/*
+ * kvtc_step_tables -- the tables of one serving step, built on the GPU from the request
+ * lengths: block table growth from a ring of free pages, the pages of finished requests
+ * back into it, and the row layout of the step's new tokens.  No counterpart on the
+ * KV-COBRA pages (paging as in PagedAttention); its outputs are what kvtc_encode_append
+ * (cu_seqlens; pos_start = cached_lens), kvtc_raw_append (slot_map, positions) and the
+ * decode calls (block table, seq_lens) read.
+ *
+ * Sequence s holds c = cached_lens[s] tokens, in pages block_table[s][0 .. ceil(c/128)),
+ * and brings n = new_lens[s] new ones (n < 0: the sequence has finished).  In sequence
+ * order:
+ *   finished: its ceil(c/128) page ids are appended to the ring's tail; seq_lens[s] = 0.
+ *     Its block table row is left as it is.  Pages given back become available from the
+ *     next call on.
+ *   otherwise: its rows are cu_seqlens[s] .. cu_seqlens[s] + n - 1; the
+ *     need = ceil((c+n)/128) - ceil(c/128) pages that it lacks are taken from the ring's
+ *     head and entered in its block table row; seq_lens[s] = c + n; row i of it gets
+ *     positions = c + i and slot_map = page * 128 + (c + i) % 128.
+ * A sequence that cannot take its tokens keeps seq_lens[s] = c (0 if c itself is out of
+ * range), no page moves for it, its rows get slot -1 and position 0, and a status bit
+ * says why: KVTC_STATUS_BAD_POS (c outside [0, max_pages * 128], c + n beyond that, or
+ * rows beyond n_rows), KVTC_STATUS_NO_PAGE (the needs of the sequences up to and
+ * including it that fit otherwise exceed the free pages; one that needs no page goes on).
+ * A negative page id met gives its rows slot -1 and sets KVTC_STATUS_BAD_PAGE.  Rows
+ * behind the last sequence's (a batch padded to n_rows) get slot -1, position 0.
+ *
+ * cached_lens, new_lens: device int32 [n_seq].  page_ring: device int32 [ring_capacity],
+ * free page ids at positions (head + i) % capacity, i < count; capacity is the number of
+ * pages in circulation (a release that would overflow it is dropped, BAD_PAGE).
+ * ring_state, ring_state_out: device int32 [2] = {head, count} before and after (a state
+ * outside the ring is read as {0, 0}, BAD_PAGE).  block_table: device int32
+ * [n_seq][max_pages], only new entries are written.  seq_lens: device int32 [n_seq].
+ * cu_seqlens: device int32 [n_seq + 1], clipped to n_rows.  slot_map: device int64
+ * [n_rows].  positions: device int32 [n_rows].  ring_state_out may be ring_state and
+ * seq_lens may be cached_lens (a loop replayed from a graph); no other two buffers may
+ * overlap.  workspace: device, 16 bytes, zero before its first use and left at zero; calls
+ * that share one must not overlap on the GPU.  status: device int32 or NULL.  n_rows may
+ * be 0 (releases only); n_seq >= 1, max_pages in [1, 2^24), ring_capacity >= 1.
+ */
+kvtc_status kvtc_step_tables(const int32_t* cached_lens, const int32_t* new_lens, int n_seq, int32_t* page_ring,
+                             int ring_capacity, const int32_t* ring_state, int32_t* block_table, int max_pages,
+                             int32_t* seq_lens, int32_t* cu_seqlens, int64_t* slot_map, int32_t* positions,
+                             int n_rows, int32_t* ring_state_out, void* workspace, int32_t* status, void* stream);
+
+/* Rotary positions of a head's 64 pairs (x_i, x_{i+64}), each driven by one position axis
+ * (time, height, width, ...). */
+#define KVTC_ROPE_MAX_AXES 4
+typedef struct {
+  int n_axes;                        /* 1 .. KVTC_ROPE_MAX_AXES                           */
+  int section[KVTC_ROPE_MAX_AXES];   /* pairs of each axis (>= 0); the first n_axes sum to 64 */
+  int interleaved;                   /* 0: axis a owns a run of section[a] pairs; 1: pairs go
+                                        round the axes that have some left (0 1 2 0 1 2 ...) */
+  double base;                       /* 0 means 500000 (as the pre-RoPE decode), else > 1 */
+} kvtc_rope_desc;
+
+/*
+ * kvtc_rope -- rotates query and key rows to their positions before the cache takes them
+ * (post-RoPE keys) or before the pre-RoPE decode (q alone), with the rotation of
+ * kvtc_decode_attention_rope: a = positions[axis(i)][row] * base^(-2i/128), i < 64,
+ *   y_i = x_i cos a - x_{i+64} sin a,   y_{i+64} = x_{i+64} cos a + x_i sin a.
+ * inverse != 0 rotates by -a: the transpose, so the gradient of x is kvtc_rope of the
+ * gradient of y with inverse set.  Angles are reduced in fp64, the rotation is fp32,
+ * rounded once.
+ * q: device, row t of head h at q + t * q_stride + h * 128 (elements of dtype: F32, BF16
+ * or F16); k likewise.  q or k may be NULL (with 0 heads).  positions: device int32
+ * [n_axes][n_tok] (any int32; a negative position rotates backwards).  q_out, k_out:
+ * device [n_tok][heads][128], contiguous; q_out may be q where q_stride = n_q_heads * 128
+ * (k likewise), no other overlap.  All row pointers 16-byte aligned, strides multiples of
+ * 16 bytes and at least heads * 128.  At most 1024 heads each.
+ */
+kvtc_status kvtc_rope(const kvtc_rope_desc* rope, const void* q, int64_t q_stride, int n_q_heads, const void* k,
+                      int64_t k_stride, int n_kv_heads, kvtc_dtype dtype, const int32_t* positions, int n_tok,
+                      int inverse, void* q_out, void* k_out, void* stream);
+
+/* ------------------------------------------------------------------ uncompressed pages -- */
+
+/*
+ * The uncompressed page cache: layers that a model keeps in 16 bits beside the coded ones,
+ * and an encoder's states.  The block table and the page size are those of the coded
+ * cache, so one table (kvtc_step_tables) serves both.  Page p of layer l holds, for every
+ * KV head h, 128 tokens of K then 128 tokens of V, rows of 128 elements:
+ *   element (l, p, h, kind, token, i) at pool + (((l * n_pages + p) * n_kv_heads + h) * 2
+ *   + kind) * 16384 + token * 128 + i.
+ * Slot number of a token = page * 128 + token.  Caller-owned; slots not yet written may
+ * hold anything.
+ */
+typedef struct {
+  void* pool;                   /* device, 128-byte aligned                          */
+  int n_layers;
+  uint64_t n_pages;             /* pages of every layer                              */
+  int n_kv_heads;
+  kvtc_dtype dtype;             /* KVTC_BF16 or KVTC_F16                             */
+  const int32_t* block_table;   /* device int32 [n_seq][max_pages] (attention calls) */
+  int n_seq;
+  int max_pages;
+  int32_t* status;              /* device int32 status word (KVTC_STATUS_*) or NULL  */
+} kvtc_raw_cache;
+
+/* Bytes of the whole pool (0 for sizes < 1). */
+uint64_t kvtc_raw_cache_bytes(int n_layers, uint64_t n_pages, int n_kv_heads);
+
+/*
+ * kvtc_raw_append -- writes K and V rows into their slots of one layer, k rotated to its
+ * position on the way (rope != NULL; the rotation of kvtc_rope, inverse = 0) and q rotated
+ * in the same pass (q != NULL, needs rope): one launch between a layer's projection and its
+ * attention.  k, v: row t of head h at k + t * k_stride + h * 128, of the cache's dtype.
+ * slot_map: device int64 [n_tok]: a negative slot is skipped (a padding row; q is rotated
+ * all the same), one beyond n_pages * 128 is skipped and sets KVTC_STATUS_BAD_PAGE.  Rows
+ * that name the same slot race.  positions, q, q_out, strides and alignment as kvtc_rope.
+ * The block table is not read (it may be NULL).
+ */
+kvtc_status kvtc_raw_append(const kvtc_raw_cache* cache, int layer, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const int64_t* slot_map, int n_tok, const kvtc_rope_desc* rope,
+                            const int32_t* positions, const void* q, int64_t q_stride, int n_q_heads, void* q_out,
+                            void* stream);
+
+/* Workspace bytes of the two attention calls below for these sizes. */
+uint64_t kvtc_raw_decode_workspace_bytes(int n_seq, int n_q_heads, int n_kv_heads, int max_seq_len);
+uint64_t kvtc_raw_cross_workspace_bytes(int n_seq, int n_tok, int n_q_heads, int n_kv_heads, int max_seq_len);
+
+/*
+ * kvtc_raw_decode_attention -- one new token per sequence over one layer's uncompressed
+ * pages: o = sum_t p_t v_t, p = softmax over t < seq_lens[s] of softmax_scale * q . k_t
+ * (0 means 1/sqrt(128)), fp32 accumulation and statistics.  Query head g of KV head h is
+ * q head h * (n_q_heads / n_kv_heads) + g, as in kvtc_decode_attention.
+ * q, out: device [n_seq][n_q_heads][128] of the cache's dtype, 16-byte aligned, no overlap
+ * with each other.  seq_lens: device int32 [n_seq]; 0 gives an all-zero output; a length
+ * outside [0, max_seq_len] sets KVTC_STATUS_BAD_POS, and a page id outside the pool among
+ * the pages read KVTC_STATUS_BAD_PAGE: the outputs of that sequence's heads are then zero.
+ * max_seq_len: host bound, at most max_pages * 128.  workspace: device, 16-byte aligned,
+ * at least kvtc_raw_decode_workspace_bytes, zero-filled before its first use; every call
+ * leaves its counters at zero again, so one workspace serves any number of consecutive
+ * calls of this function that fit it, but calls that share a workspace and overlap on the
+ * GPU race.  At most 1024 query heads per KV head.
+ */
+kvtc_status kvtc_raw_decode_attention(const kvtc_raw_cache* cache, int layer, const void* q, int n_q_heads,
+                                      const int32_t* seq_lens, int max_seq_len, float softmax_scale, void* out,
+                                      void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * kvtc_raw_cross_attention -- attention of many query rows to states of another length:
+ * rows cu_q[s] .. cu_q[s+1]-1 of q attend, without a causal mask, to the first
+ * seq_lens[s] tokens of sequence s's pages (an encoder's states, written once by
+ * kvtc_raw_append).  Scale, head order, errors, empty sequences and the workspace as
+ * kvtc_raw_decode_attention (workspace bytes: kvtc_raw_cross_workspace_bytes).
+ * q, out: device [n_tok][n_q_heads][128] of the cache's dtype, 16-byte aligned, no overlap.
+ * cu_q: device int32 [n_seq + 1], non-decreasing from >= 0; rows outside
+ * [cu_q[0], cu_q[n_seq]) are left as they were.  A sequence whose rows reach outside
+ * [0, n_tok] or run backwards is skipped and sets KVTC_STATUS_BAD_POS.  At most 128 query
+ * heads per KV head.
+ */
+kvtc_status kvtc_raw_cross_attention(const kvtc_raw_cache* cache, int layer, const void* q, int n_q_heads,
+                                     const int32_t* cu_q, int n_tok, const int32_t* seq_lens, int max_seq_len,
+                                     float softmax_scale, void* out, void* workspace, uint64_t workspace_bytes,
+                                     void* stream);
 
 #ifdef __cplusplus
 }
