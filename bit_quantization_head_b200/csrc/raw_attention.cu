@@ -1,4 +1,4 @@
-// kvtc_raw_decode_attention and kvtc_raw_cross_attention, plainly: a warp per query row and
+// kvtc_raw_cross_attention, plainly: a warp per query row and
 // head walks its sequence's tokens with the running maximum and sum of the softmax.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -128,30 +128,10 @@ kvtc_status run(const kvtc_raw_cache* c, int layer, const void* q, int n_q_heads
 
 using namespace kvtc;
 
-extern "C" uint64_t kvtc_raw_decode_workspace_bytes(int n_seq, int n_q_heads, int n_kv_heads, int max_seq_len) {
-  if (n_seq < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || max_seq_len < 0) return 0;
-  return 16;
-}
-
 extern "C" uint64_t kvtc_raw_cross_workspace_bytes(int n_seq, int n_tok, int n_q_heads, int n_kv_heads,
                                                    int max_seq_len) {
   if (n_seq < 1 || n_tok < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads || max_seq_len < 0) return 0;
   return 16;
-}
-
-extern "C" kvtc_status kvtc_raw_decode_attention(const kvtc_raw_cache* cache, int layer, const void* q, int n_q_heads,
-                                                 const int32_t* seq_lens, int max_seq_len, float softmax_scale,
-                                                 void* out, void* workspace, uint64_t workspace_bytes, void* stream) {
-  kvtc_status st = raw::check_attention(cache, layer, n_q_heads, 1024, max_seq_len, softmax_scale);
-  if (st != KVTC_OK) return st;
-  if (!q || !seq_lens || !out || !workspace) return fail(KVTC_EINVAL, "null device pointer");
-  if (!raw::aligned16(q) || !raw::aligned16(out) || !raw::aligned16(workspace))
-    return fail(KVTC_EINVAL, "q, out and workspace must be 16-byte aligned");
-  if (workspace_bytes < kvtc_raw_decode_workspace_bytes(cache->n_seq, n_q_heads, cache->n_kv_heads, max_seq_len))
-    return fail(KVTC_ECAPACITY, "decode workspace too small");
-  if (raw::overlap(q, out, static_cast<uint64_t>(cache->n_seq) * n_q_heads * kD * 2))
-    return fail(KVTC_EINVAL, "out overlaps q");
-  return run(cache, layer, q, n_q_heads, nullptr, cache->n_seq, seq_lens, max_seq_len, softmax_scale, out, stream);
 }
 
 extern "C" kvtc_status kvtc_raw_cross_attention(const kvtc_raw_cache* cache, int layer, const void* q, int n_q_heads,

@@ -1,6 +1,7 @@
 // Shared by the calls around the cache and on the uncompressed pages: argument checks, the
 // current device's SM count and launches with programmatic stream serialization.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -72,6 +73,15 @@ inline kvtc_status sm_count(int* out) {
   *out = n;
   return KVTC_OK;
 }
+
+// The pool as a 2-D tensor of rows (128 elements), loaded in 128-byte-swizzled boxes of 64
+// elements x box_rows rows; row of (layer, page, head, kind, token) = (((layer * n_pages +
+// page) * n_kv_heads + head) * 2 + kind) * 128 + token (raw_decode.cu).
+kvtc_status pool_map(CUtensorMap* m, const kvtc_raw_cache* c, int box_rows);
+// [n_tok][n_q_heads][128] queries as (element, head of the group, KV head, token), in
+// swizzled boxes of 64 elements x box_heads x 1 x box_tok.
+kvtc_status query_map(CUtensorMap* m, const void* q, kvtc_dtype dtype, int n_tok, int n_kv_heads, int group,
+                      int box_heads, int box_tok);
 
 // Launch that may start while the previous kernel of the stream finishes; the kernel calls
 // griddepcontrol.wait before it touches memory.
