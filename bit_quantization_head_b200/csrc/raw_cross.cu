@@ -1,0 +1,782 @@
+// kvtc_raw_cross_attention: ragged query rows over an encoder's states in uncompressed pages.
+//
+// o = sum_t p_t v_t / sum_t p_t with p_t = 2^(c (q . k_t - m)), c = scale * log2(e), in one
+// pass with a running reference m and the running sum of every row.  m follows the maximum
+// only when a row's score exceeds it by more than 2^8 in p: the sum and the accumulators are
+// scaled then, otherwise not at all.
+//
+// Bound: the tensor cores (512 flops per query row, head and token); for few rows the bytes
+// of the states.  S = Q K^T and O += P V run on tcgen05 (M = 128 rows, N = 128), both
+// accumulators and P (16 bits, over S's columns) in TMEM.
+//
+// Rows of a tile: the tokens' query heads of one KV head (token-major, as many whole tokens
+// as fit in 128 rows), so K and V are read once for all of them.  A unit is (sequence, KV
+// head, two such tiles); a step is its 128-token K and V page against both.  All steps of
+// all units in a row are cut into one equal run per CTA (one CTA per SM), found on the
+// device from cu_q and seq_lens; a unit that several CTAs share leaves (m, l, O) of each
+// part in the workspace, and the last CTA to arrive joins them in order, so results do not
+// depend on timing.
+//
+// CTA: warps 0-3 and 4-7 hold one row per thread of the first and second tile (softmax,
+// rescaling, output), warp 8 loads with TMA, one thread of warp 9 issues the MMAs in the
+// order PV_a(j), S_a(j+1), PV_b(j), S_b(j+1): one tile's softmax runs beside the other's
+// MMAs.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "ptx.cuh"
+#include "raw_cache.cuh"
+#include "raw_device.cuh"
+
+namespace kvtc {
+namespace raw {
+namespace {
+
+constexpr int kRows = 128;                       // rows of a tile (TMEM lanes)
+constexpr int kWarps = 12;                       // the last two idle: register shares go by four warps
+constexpr int kThreads = 32 * kWarps;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kHalfBytes = 128 * 128;       // 64 elements of 128 rows
+constexpr uint32_t kTileBytes = 2 * kHalfBytes;
+constexpr int kStages = 5;                       // K or V tiles in flight
+constexpr int kMaxCtas = 160;                    // partial slots in the workspace
+constexpr int kPartFloats = kRows * (kD + 2);    // (m, l) of each row, then its sums
+constexpr uint32_t kTmemCols = 512;              // S_a, S_b, O_a, O_b
+// Registers of a thread: 384 threads start with 168 each (64512); the row warps take what
+// the others leave (2 * 216 + 72 = 3 * 168).
+constexpr int kRowRegs = 216, kOtherRegs = 72;
+constexpr float kSlack = 8.0f;                   // log2 of what p may reach before m moves
+
+// The part of a unit that this CTA computes.
+struct Part {
+  int steps;        // 128-token steps (0: no tokens or a bad page)
+  int tail;         // tokens of the last step
+  int tok0, tok1;   // query tokens of the unit
+  int head;         // KV head
+  int two;          // whether the second tile has rows
+  int first, last;  // whether the part holds the unit's first and last step
+  int bad;
+  int c0, c1;       // CTAs that share the unit
+  int end;          // last part of the run
+};
+
+struct __align__(1024) Smem {
+  unsigned char q[2][kTileBytes];
+  unsigned char kv[kStages][kTileBytes];
+  Part part[2];
+  uint64_t kv_full[kStages], kv_empty[kStages], q_full, q_empty, part_full[2], part_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2], join[2], drain;
+  long long warp_sum[kWarps];
+  int warp_max[kWarps];
+  long long first_step, total;
+  int first_seq;
+  int dead;
+  int last_in[2];
+  uint32_t tmem;
+};
+
+static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory of a CTA");
+
+struct CrossArgs {
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  int n_seq, max_pages, max_len, n_tok;
+  long long n_pages;
+  int H, G;
+  int tile_tok;      // query tokens of a tile
+  int row0;          // first pool row of the layer
+  uint16_t* out;
+  float c;           // scale * log2(e)
+  int* tickets;
+  float* parts;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// 32 columns of this warp's lanes, not waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Shared-memory matrix descriptors, 128-byte swizzle (layout type 2, version 1).  K-major
+// rows of 128 bytes: 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// N-major (V: tokens are K): 64-element column blocks kHalfBytes apart, 8-token groups 1024
+// bytes apart.
+__device__ __forceinline__ uint64_t desc_n(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(kHalfBytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// fp32 accumulate, bf16 or f16 operands, M = N = 128; B N-major for the value product.
+template <bool F16>
+__device__ __forceinline__ constexpr uint32_t idesc(bool b_n_major) {
+  return (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (b_n_major ? 1u << 16 : 0u) | ((128u >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// A sequence as the kernel uses it: its query rows, tokens, units per KV head and steps.
+struct Seq {
+  int tok0, tok1, len, blocks, steps;
+  bool bad;
+};
+__device__ __forceinline__ Seq seq_of(const CrossArgs& a, int s) {
+  Seq q;
+  q.tok0 = a.cu_q[s];
+  q.tok1 = a.cu_q[s + 1];
+  q.len = a.seq_lens[s];
+  q.bad = false;
+  q.blocks = 0;
+  if (q.tok0 < 0 || q.tok1 < q.tok0 || q.tok1 > a.n_tok) {
+    q.bad = true;
+  } else {
+    q.blocks = (q.tok1 - q.tok0 + 2 * a.tile_tok - 1) / (2 * a.tile_tok);
+    if (q.len < 0 || q.len > a.max_len) q.bad = true, q.len = 0;
+  }
+  q.steps = max(1, (q.len + kPage - 1) / kPage);
+  return q;
+}
+
+// ------------------------------------------------------------------ loads (one warp)
+__device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map, const CUtensorMap* q_map,
+                          long long f, long long f1, int n_cta) {
+  const int lane = threadIdx.x & 31;
+  volatile int* dead = &s.dead;
+  int seq = s.first_seq, n_part = 0, n_q = 0, it = 0;
+  long long base = s.first_step;  // first step of the sequence's units
+  Seq sq = seq_of(a, seq);
+  uint32_t flags = 0;
+  bool ok = true;
+  auto load = [&](int row) {  // the 128 rows from `row` into the next stage (lane 0)
+    const int st = it % kStages;
+    if (it >= kStages && !wait_phase(&s.kv_empty[st], (it / kStages - 1) & 1, dead)) return false;
+    mbar_arrive_expect_tx(&s.kv_full[st], kTileBytes);
+    tma_load_2d(s.kv[st], kv_map, 0, row, &s.kv_full[st]);
+    tma_load_2d(s.kv[st] + kHalfBytes, kv_map, 64, row, &s.kv_full[st]);
+    ++it;
+    return true;
+  };
+  while (f < f1 && ok) {
+    while (f >= base + static_cast<long long>(sq.steps) * a.H * sq.blocks) {
+      base += static_cast<long long>(sq.steps) * a.H * sq.blocks;
+      sq = seq_of(a, ++seq);
+    }
+    const int u = static_cast<int>((f - base) / sq.steps), h = u / sq.blocks, blk = u - h * sq.blocks;
+    const long long begin = base + static_cast<long long>(u) * sq.steps;
+    const int i0 = static_cast<int>(f - begin);
+    const int i1 = static_cast<int>(min(static_cast<long long>(sq.steps), i0 + (f1 - f)));
+    const int32_t* pages = a.table + static_cast<size_t>(seq) * a.max_pages;
+    bool good = true;
+    if (sq.len > 0)
+      for (int p = i0 + lane; p < i1; p += 32) {
+        const int id = pages[p];
+        good &= id >= 0 && id < a.n_pages;
+      }
+    good = __all_sync(0xffffffffu, good);
+    if (!good) flags |= KVTC_STATUS_BAD_PAGE;
+    const int steps = good && sq.len > 0 ? i1 - i0 : 0;
+    Part d;
+    d.steps = steps;
+    d.tail = sq.len - (sq.steps - 1) * kPage;
+    d.tok0 = sq.tok0 + blk * 2 * a.tile_tok;
+    d.tok1 = min(sq.tok1, d.tok0 + 2 * a.tile_tok);
+    d.head = h;
+    d.two = d.tok1 - d.tok0 > a.tile_tok;
+    d.first = i0 == 0;
+    d.last = i1 == sq.steps;
+    d.bad = !good;
+    d.c0 = run_owner(begin, n_cta, s.total);
+    d.c1 = run_owner(begin + sq.steps - 1, n_cta, s.total);
+    f += i1 - i0;
+    d.end = f >= f1;
+    if (lane == 0) {
+      if (n_part >= 2) ok = wait_phase(&s.part_empty[n_part & 1], ((n_part >> 1) - 1) & 1, dead);
+      if (ok) {
+        s.part[n_part & 1] = d;
+        mbar_arrive(&s.part_full[n_part & 1]);
+      }
+    }
+    ++n_part;
+    int ids = 0;
+    for (int i = i0; i < i0 + steps; ++i) {
+      if (((i - i0) & 31) == 0) ids = i + lane < i1 ? pages[i + lane] : 0;
+      const int id = __shfl_sync(0xffffffffu, ids, (i - i0) & 31);
+      if (lane == 0 && ok) {
+        const int row = a.row0 + (id * a.H + h) * 2 * kPage;
+        ok = load(row);
+        if (ok && i == i0) {
+          if (n_q > 0) ok = wait_phase(&s.q_empty, (n_q - 1) & 1, dead);
+          if (ok) {
+            const uint32_t bytes = static_cast<uint32_t>(a.tile_tok * a.G) * 128u;  // of one half of one tile
+            mbar_arrive_expect_tx(&s.q_full, bytes * (d.two ? 4u : 2u));
+            for (int x = 0; x <= d.two; ++x) {
+              tma_load_4d(s.q[x], q_map, 0, 0, h, d.tok0 + x * a.tile_tok, &s.q_full);
+              tma_load_4d(s.q[x] + kHalfBytes, q_map, 64, 0, h, d.tok0 + x * a.tile_tok, &s.q_full);
+            }
+            ++n_q;
+          }
+        }
+        ok = ok && load(row + kPage);
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  }
+  if (lane == 0) {
+    if (!ok) {
+      *dead = 1;
+      flags |= KVTC_STATUS_TIMEOUT;
+    }
+    if (flags && a.status) atomicOr(a.status, static_cast<int>(flags));
+    // every copy in flight lands before the CTA may exit (bounded)
+    volatile int never = 0;
+    for (int k = max(0, it - kStages); k < it; ++k) (void)wait_phase(&s.kv_full[k % kStages], (k / kStages) & 1, &never);
+    if (n_q > 0) (void)wait_phase(&s.q_full, (n_q - 1) & 1, &never);
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ MMAs (one thread)
+template <bool F16>
+__device__ void mma_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
+  volatile int* dead = &s.dead;
+  int it = 0, n_q = 0, n_p[2] = {0, 0};
+  auto scores = [&](int x, int st) {
+    const uint32_t q = smem_u32(s.q[x]), k = smem_u32(s.kv[st]);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;  // 16 elements = 32 bytes
+      mma_ss(tmem + x * 128, desc_k(q + off), desc_k(k + off), idesc<F16>(false), kk > 0);
+    }
+    tc_commit(&s.s_full[x]);
+  };
+  bool ok = true;
+  for (int n = 0;; ++n) {
+    if (!(ok = wait_phase(&s.part_full[n & 1], (n >> 1) & 1, dead))) break;
+    const Part d = s.part[n & 1];
+    mbar_arrive(&s.part_empty[n & 1]);
+    if (d.steps > 0) {
+      if (!(ok = wait_phase(&s.q_full, n_q & 1, dead))) break;
+      ++n_q;
+      if (!(ok = wait_phase(&s.kv_full[it % kStages], (it / kStages) & 1, dead))) break;
+      tc_fence_after();
+      for (int x = 0; x <= d.two; ++x) scores(x, it % kStages);
+      tc_commit(&s.kv_empty[it % kStages]);
+      if (d.steps == 1) tc_commit(&s.q_empty);
+    }
+    for (int j = 0; j < d.steps && ok; ++j, it += 2) {
+      const int vs = (it + 1) % kStages, ks = (it + 2) % kStages;
+      const bool more = j + 1 < d.steps;
+      if (!(ok = wait_phase(&s.kv_full[vs], ((it + 1) / kStages) & 1, dead))) break;
+      // tokens past the end add nothing: only their groups of 16 that hold a token
+      const int groups = d.last && !more ? (d.tail + 15) >> 4 : 8;
+      for (int x = 0; x <= d.two && ok; ++x) {
+        if (!(ok = wait_phase(&s.p_full[x], n_p[x]++ & 1, dead))) break;
+        tc_fence_after();
+        const uint32_t v = smem_u32(s.kv[vs]);
+        for (int g = 0; g < groups; ++g)
+          mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * g, desc_n(v + g * 2048), idesc<F16>(true), j > 0 || g > 0);
+        if (x == d.two) tc_commit(&s.kv_empty[vs]);
+        if (!more) {
+          tc_commit(&s.o_full[x]);
+        } else {
+          if (x == 0) {
+            if (!(ok = wait_phase(&s.kv_full[ks], ((it + 2) / kStages) & 1, dead))) break;
+            tc_fence_after();
+          }
+          scores(x, ks);
+          if (x == d.two) {
+            tc_commit(&s.kv_empty[ks]);
+            if (j + 2 == d.steps) tc_commit(&s.q_empty);
+          }
+        }
+      }
+    }
+    if (!ok || d.end) break;
+  }
+  if (!ok) {
+    *dead = 1;
+    if (a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_TIMEOUT));
+  }
+  // the MMAs issued complete before TMEM is freed (bounded)
+  volatile int never = 0;
+  tc_commit(&s.drain);
+  (void)wait_phase(&s.drain, 0, &never);
+}
+
+// ------------------------------------------------------------------ rows (four warps a tile)
+// Partial slot of CTA c and tile x.  Slot 1 holds the unit that begins in the CTA, slot 0
+// the one that came from an earlier CTA.
+__device__ __forceinline__ float* part_of(const CrossArgs& a, int c, int slot, int x) {
+  return a.parts + static_cast<size_t>((c * 2 + slot) * 2 + x) * kPartFloats;
+}
+
+template <bool F16>
+__device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int x = warp >> 2, row = threadIdx.x & 127;
+  // fp16 weights: 2^7 at the reference, so those far below it keep clear of the subnormals
+  // and 2^(7 + kSlack) stays in range
+  constexpr float kBias = F16 ? 7.0f : 0.0f;
+  volatile int* dead = &s.dead;
+  const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
+  const int tok_in = row / a.G, head_in = row - tok_in * a.G;
+  const uint64_t c2 = pair(a.c, a.c);
+  uint32_t join_phase = 0;
+  int it = 0, n_s = 0, n_o = 0;
+  auto give_up = [&] {
+    if (lane == 0) {
+      *dead = 1;
+      if (a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_TIMEOUT));
+    }
+  };
+  auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
+    const bool ok = __all_sync(0xffffffffu, wait_phase(bar, phase, dead));
+    if (!ok) give_up();
+    return ok;
+  };
+  // Barrier of the tile's four warps.
+  auto tile_sync = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.join[x]);
+    join_phase ^= 1;
+    return wait(&s.join[x], join_phase ^ 1);
+  };
+  for (int n = 0;; ++n) {
+    if (!wait(&s.part_full[n & 1], (n >> 1) & 1)) return;
+    const Part d = s.part[n & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.part_empty[n & 1]);
+    if (x == 0 || d.two) {
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < d.steps; ++j) {
+        const int valid = d.last && j == d.steps - 1 ? d.tail : kPage;
+        if (!wait(&s.s_full[x], n_s++ & 1)) return;
+        tc_fence_after();
+        float sc[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, sc + 32 * i);
+        tmem_wait_ld();
+        if (valid < kPage) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= valid) sc[i] = -INFINITY;
+          if (x == 0 && (valid & 15)) {
+            // V rows past the end may hold anything (0 * NaN is NaN): clear those that the
+            // last group of 16 tokens takes in
+            const int vi = it + 2 * j + 1, st = vi % kStages;
+            if (!wait(&s.kv_full[st], (vi / kStages) & 1)) return;
+            for (int e = row; e < (16 - (valid & 15)) * 16; e += 128) {
+              const int r = valid + (e >> 4);
+              *reinterpret_cast<uint4*>(s.kv[st] + ((e >> 3) & 1) * kHalfBytes + r * 128 + (e & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        float t0 = sc[0], t1 = sc[1], t2 = sc[2], t3 = sc[3];
+#pragma unroll
+        for (int i = 4; i < 124; i += 8) {
+          t0 = max3(t0, sc[i], sc[i + 1]);
+          t1 = max3(t1, sc[i + 2], sc[i + 3]);
+          t2 = max3(t2, sc[i + 4], sc[i + 5]);
+          t3 = max3(t3, sc[i + 6], sc[i + 7]);
+        }
+        t0 = max3(t0, sc[124], sc[125]);
+        t1 = max3(t1, sc[126], sc[127]);
+        const float top = fmaxf(max3(t0, t1, t2), t3);
+        if (__any_sync(0xffffffffu, (top - m) * a.c > kSlack)) {
+          const float to_m = fmaxf(m, top);
+          const float f = m == -INFINITY ? 0.0f : ex2((m - to_m) * a.c);
+          l *= f;
+          m = to_m;
+          if (j > 0) {
+            // S(j) was issued after PV(j - 1), so the accumulators are complete
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float o[32];
+              uint32_t w[32];
+              tmem_ld32(to + 32 * i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+              tmem_st32(to + 32 * i, w);
+            }
+          }
+        }
+        const float neg = kBias - m * a.c;
+        const uint64_t neg2 = pair(neg, neg);
+        uint64_t sum0 = pair(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = 64 * hf + 2 * i;
+            float lo, hi;
+            unpair(fma2(pair(sc[e], sc[e + 1]), c2, neg2), lo, hi);
+            lo = ex2(lo);
+            hi = ex2(hi);
+            if (i & 1)
+              sum1 = add2(sum1, pair(lo, hi));
+            else
+              sum0 = add2(sum0, pair(lo, hi));
+            // P enters the value product in the pages' type (half a step of relative error
+            // on each weight, as for the output; the sum l stays fp32)
+            w[i] = pack2<F16>(lo, hi);
+          }
+          tmem_st32(ts + 32 * hf, w);
+        }
+        float a0, a1;
+        unpair(add2(sum0, sum1), a0, a1);
+        l += a0 + a1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.p_full[x]);
+      }
+      if (d.steps > 0) {
+        if (!wait(&s.o_full[x], n_o++ & 1)) return;
+        tc_fence_after();
+      }
+      const int tok = d.tok0 + x * a.tile_tok + tok_in;
+      const bool live = tok_in < a.tile_tok && tok < d.tok1;
+      uint16_t* dst = a.out + (static_cast<size_t>(tok) * a.H * a.G + static_cast<size_t>(d.head) * a.G + head_in) * kD;
+      const bool whole = d.first && d.last;
+      float* mine = part_of(a, blockIdx.x, d.first, x);
+      const float r = whole && d.steps > 0 ? 1.0f / l : 0.0f;
+      if (!whole && live) reinterpret_cast<float2*>(mine)[row] = make_float2(m, d.bad ? -1.0f : l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float o[32];
+        __syncwarp();
+        if (d.steps > 0) {
+          tmem_ld32(to + 32 * i, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+        }
+        if (!live) continue;
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = pack2<F16>(o[e] * r, o[e + 1] * r);
+            w.y = pack2<F16>(o[e + 2] * r, o[e + 3] * r);
+            w.z = pack2<F16>(o[e + 4] * r, o[e + 5] * r);
+            w.w = pack2<F16>(o[e + 6] * r, o[e + 7] * r);
+            reinterpret_cast<uint4*>(dst + 32 * i + e)[0] = w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            reinterpret_cast<float4*>(mine + 2 * kRows)[(8 * i + e / 4) * kRows + row] =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (!whole) {
+        // ---- the unit is shared with other CTAs: the last one to arrive joins the parts
+        __threadfence();
+        if (!tile_sync()) return;
+        if (row == 0) s.last_in[x] = atomicAdd(a.tickets + 2 * d.c0 + x, 1) == d.c1 - d.c0;
+        if (!tile_sync()) return;
+        if (s.last_in[x]) {
+          __threadfence();
+          if (row == 0) a.tickets[2 * d.c0 + x] = 0;
+          if (live) {
+            float top = -INFINITY;
+            bool bad = false;
+            for (int c = d.c0; c <= d.c1; ++c) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(a, c, c == d.c0, x)) + row);
+              top = fmaxf(top, ml.x);
+              bad |= ml.y < 0.0f;
+            }
+            float sum = 0.0f, o[128];
+#pragma unroll
+            for (int e = 0; e < 128; ++e) o[e] = 0.0f;
+            for (int c = d.c0; c <= d.c1 && !bad; ++c) {
+              const float* p = part_of(a, c, c == d.c0, x);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p) + row);
+              const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
+              sum += ml.y * f;
+#pragma unroll
+              for (int e = 0; e < 128; e += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows) + (e / 4) * kRows + row);
+                o[e] += v.x * f, o[e + 1] += v.y * f, o[e + 2] += v.z * f, o[e + 3] += v.w * f;
+              }
+            }
+            const float rs = bad ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int e = 0; e < 128; e += 8) {
+              uint4 w;
+              w.x = pack2<F16>(o[e] * rs, o[e + 1] * rs);
+              w.y = pack2<F16>(o[e + 2] * rs, o[e + 3] * rs);
+              w.z = pack2<F16>(o[e + 4] * rs, o[e + 5] * rs);
+              w.w = pack2<F16>(o[e + 6] * rs, o[e + 7] * rs);
+              reinterpret_cast<uint4*>(dst + e)[0] = w;
+            }
+          }
+        }
+      }
+    }
+    it += 2 * d.steps;
+    if (d.end) return;
+  }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    raw_cross_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
+                     const __grid_constant__ CrossArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.kv_empty[i], 1);
+    }
+    mbar_init(&s.q_full, 1);
+    mbar_init(&s.q_empty, 1);
+    mbar_init(&s.drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.part_full[i], 1);
+      mbar_init(&s.part_empty[i], 9);  // the eight row warps and the MMA thread
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.o_full[i], 1);
+      mbar_init(&s.join[i], 4);
+    }
+    s.dead = 0;
+    fence_mbar_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  // steps of all sequences (thread i: the i-th share of them), the longest sequence, and
+  // the sequence of this CTA's first step
+  const int per = (a.n_seq + kThreads - 1) / kThreads;
+  const int s0 = min(a.n_seq, tid * per), s1 = min(a.n_seq, s0 + per);
+  long long mine = 0;
+  int longest = 0;
+  bool bad = false;
+  for (int i = s0; i < s1; ++i) {
+    const Seq q = seq_of(a, i);
+    bad |= q.bad;
+    mine += static_cast<long long>(q.steps) * q.blocks;
+    if (q.blocks) longest = max(longest, q.steps);
+  }
+  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_BAD_POS));
+  mine *= a.H;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    s.warp_sum[warp] = incl;
+    s.warp_max[warp] = longest;
+  }
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s.warp_sum[w];
+    total += s.warp_sum[w];
+    longest = max(longest, s.warp_max[w]);
+  }
+  // A run of r steps saves (longest / r) joins of about half a step each at the end of a
+  // unit: no run shorter than sqrt(longest / 2).
+  const int shortest = max(1, static_cast<int>(sqrtf(0.5f * static_cast<float>(longest))));
+  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + shortest - 1) / shortest));
+  if (static_cast<int>(blockIdx.x) >= n_cta) return;  // the whole CTA
+  const long long f0 = run_start(blockIdx.x, n_cta, total), f1 = run_start(blockIdx.x + 1, n_cta, total);
+  if (before <= f0 && f0 < before + mine) {
+    long long b = before;
+    int i = s0;
+    for (; i < s1 - 1; ++i) {
+      const Seq q = seq_of(a, i);
+      const long long n = static_cast<long long>(q.steps) * q.blocks * a.H;
+      if (f0 < b + n) break;
+      b += n;
+    }
+    s.first_seq = i;
+    s.first_step = b;
+    s.total = total;
+  }
+  __syncwarp();
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&s.tmem)),
+                 "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem;
+  if (warp >= kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) load_role(a, s, &kv_map, &q_map, f0, f1, n_cta);
+    if (warp == kMmaWarp && lane == 0) mma_role<F16>(a, s, tmem);
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRowRegs));
+    row_role<F16>(a, s, tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(kTmemCols) : "memory");
+}
+
+// CTAs that a call can use: no more than it has steps.
+int grid_bound(int n_seq, int n_tok, int n_kv_heads, int group, int max_seq_len) {
+  const long long tile_tok = std::max(1, kRows / group);
+  const long long blocks = n_tok / (2 * tile_tok) + n_seq;
+  const long long steps = std::max(1, (max_seq_len + kPage - 1) / kPage);
+  if (blocks >= kMaxCtas || steps >= kMaxCtas || n_kv_heads >= kMaxCtas) return kMaxCtas;
+  return static_cast<int>(std::min<long long>(kMaxCtas, blocks * steps * n_kv_heads));
+}
+
+template <bool F16>
+kvtc_status launch_cross(const CUtensorMap& kv_map, const CUtensorMap& q_map, const CrossArgs& a, int grid,
+                         void* stream) {
+  const size_t smem = sizeof(Smem) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(raw_cross_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (raw cross)");
+  e = launch(raw_cross_kernel<F16>, dim3(static_cast<unsigned>(grid)), kThreads, smem, stream, kv_map, q_map, a);
+  if (e != cudaSuccess) return cuda_fail(e, "raw cross launch");
+  return KVTC_OK;
+}
+
+}  // namespace
+}  // namespace raw
+}  // namespace kvtc
+
+using namespace kvtc;
+
+// Counters of the CTAs (4096 bytes), then two slots of two tiles for each.
+extern "C" uint64_t kvtc_raw_cross_workspace_bytes(int n_seq, int n_tok, int n_q_heads, int n_kv_heads,
+                                                   int max_seq_len) {
+  if (n_seq < 1 || n_tok < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads || max_seq_len < 0) return 0;
+  const int ctas = raw::grid_bound(n_seq, n_tok, n_kv_heads, std::min(raw::kRows, n_q_heads / n_kv_heads), max_seq_len);
+  return 4096 + static_cast<uint64_t>(ctas) * 4 * raw::kPartFloats * sizeof(float);
+}
+
+extern "C" kvtc_status kvtc_raw_cross_attention(const kvtc_raw_cache* cache, int layer, const void* q, int n_q_heads,
+                                                const int32_t* cu_q, int n_tok, const int32_t* seq_lens,
+                                                int max_seq_len, float softmax_scale, void* out, void* workspace,
+                                                uint64_t workspace_bytes, void* stream) {
+  kvtc_status st = raw::check_attention(cache, layer, n_q_heads, raw::kRows, max_seq_len, softmax_scale);
+  if (st != KVTC_OK) return st;
+  if (n_tok < 0) return fail(KVTC_EINVAL, "n_tok must be >= 0");
+  if (n_tok == 0) return KVTC_OK;
+  if (!q || !cu_q || !seq_lens || !out || !workspace) return fail(KVTC_EINVAL, "null device pointer");
+  if (!raw::aligned16(q) || !raw::aligned16(out) || !raw::aligned16(workspace))
+    return fail(KVTC_EINVAL, "q, out and workspace must be 16-byte aligned");
+  if (workspace_bytes < kvtc_raw_cross_workspace_bytes(cache->n_seq, n_tok, n_q_heads, cache->n_kv_heads, max_seq_len))
+    return fail(KVTC_ECAPACITY, "cross attention workspace too small");
+  if (raw::overlap(q, out, static_cast<uint64_t>(n_tok) * n_q_heads * kD * 2))
+    return fail(KVTC_EINVAL, "out overlaps q");
+  int sms = 0;
+  st = raw::sm_count(&sms);
+  if (st != KVTC_OK) return st;
+  raw::CrossArgs a;
+  a.table = cache->block_table;
+  a.seq_lens = seq_lens;
+  a.cu_q = cu_q;
+  a.n_seq = cache->n_seq;
+  a.max_pages = cache->max_pages;
+  a.max_len = max_seq_len;
+  a.n_tok = n_tok;
+  a.n_pages = static_cast<long long>(cache->n_pages);
+  a.H = cache->n_kv_heads;
+  a.G = n_q_heads / cache->n_kv_heads;
+  a.tile_tok = raw::kRows / a.G;
+  a.row0 = static_cast<int>(static_cast<uint64_t>(layer) * cache->n_pages * static_cast<uint64_t>(a.H) * 2 * kPage);
+  a.out = static_cast<uint16_t*>(out);
+  a.c = (softmax_scale > 0.0f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(kD))) * 1.4426950408889634f;
+  a.tickets = static_cast<int*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + 4096);
+  a.status = cache->status;
+  CUtensorMap kv_map, q_map;
+  st = raw::pool_map(&kv_map, cache, kPage);
+  if (st == KVTC_OK) st = raw::query_map(&q_map, q, cache->dtype, n_tok, a.H, a.G, a.G, a.tile_tok);
+  if (st != KVTC_OK) return st;
+  const int grid = std::min(sms, raw::grid_bound(a.n_seq, n_tok, a.H, a.G, max_seq_len));
+  return cache->dtype == KVTC_F16 ? raw::launch_cross<true>(kv_map, q_map, a, grid, stream)
+                                  : raw::launch_cross<false>(kv_map, q_map, a, grid, stream);
+}

@@ -29,6 +29,7 @@
 
 #include "ptx.cuh"
 #include "raw_cache.cuh"
+#include "raw_device.cuh"
 
 namespace kvtc {
 namespace raw {
@@ -85,12 +86,6 @@ struct DecodeArgs {
   int32_t* status;
 };
 
-// Tile at which CTA i of n starts, and the CTA that holds tile t.
-__device__ __forceinline__ long long run_start(long long i, long long n, long long total) { return i * total / n; }
-__device__ __forceinline__ int run_owner(long long t, long long n, long long total) {
-  return static_cast<int>(((t + 1) * n + total - 1) / total) - 1;
-}
-
 // Length of sequence s as the kernel uses it, and whether it is out of range.
 __device__ __forceinline__ int seq_len(const DecodeArgs& a, int s, bool& bad) {
   const int n = a.seq_lens[s];
@@ -99,13 +94,6 @@ __device__ __forceinline__ int seq_len(const DecodeArgs& a, int s, bool& bad) {
 }
 __device__ __forceinline__ int n_tiles(int len) { return max(1, (len + kTile - 1) / kTile); }
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -128,23 +116,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if (F16) return pack_half2(lo, hi);
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Bounded wait (2^16 sleeps of up to 20 us), given up at once when the CTA is dead.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t phase, volatile int* dead) {
-  if (mbar_try_wait(bar, phase)) return true;
-  for (uint32_t i = 0; i < (1u << 16); ++i) {
-    if (mbar_try_wait_sleep(bar, phase, 20000u)) return true;
-    if (*dead) return false;
-  }
-  return false;
-}
-
 // ------------------------------------------------------------------ producer warp
 template <int NT>
 __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map, long long f, long long f1, int n_cta) {

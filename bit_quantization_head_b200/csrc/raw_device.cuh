@@ -1,0 +1,54 @@
+// Device helpers of the two attention kernels on the uncompressed pages.
+#pragma once
+#include <cuda.h>
+
+#include "ptx.cuh"
+#include "raw_cache.cuh"
+
+namespace kvtc {
+namespace raw {
+
+// All tiles of all units in a row, cut into one run per CTA: the tile at which CTA i of n
+// starts, and the CTA that holds tile t.
+__device__ __forceinline__ long long run_start(long long i, long long n, long long total) { return i * total / n; }
+__device__ __forceinline__ int run_owner(long long t, long long n, long long total) {
+  return static_cast<int>(((t + 1) * n + total - 1) / total) - 1;
+}
+
+// Bounded wait (2^16 sleeps of up to 20 us), given up at once when the CTA is dead.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t phase, volatile int* dead) {
+  if (mbar_try_wait(bar, phase)) return true;
+  for (uint32_t i = 0; i < (1u << 16); ++i) {
+    if (mbar_try_wait_sleep(bar, phase, 20000u)) return true;
+    if (*dead) return false;
+  }
+  return false;
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Two floats rounded to the pages' type.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (F16) return pack_half2(lo, hi);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace raw
+}  // namespace kvtc
