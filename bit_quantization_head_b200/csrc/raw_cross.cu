@@ -98,9 +98,19 @@ struct CrossArgs {
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
-               : "memory");
+// The MMA warp runs its role as a whole (uniform control and addresses); `one` is set in the
+// lane that issues.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
 }
 // 32 columns of this warp's lanes, not waited for.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -129,35 +139,40 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-// Shared-memory matrix descriptors, 128-byte swizzle (layout type 2, version 1).  K-major
-// rows of 128 bytes: 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// Shared-memory matrix descriptors, 128-byte swizzle (layout type 2, version 1), 8-row
+// groups 1024 bytes apart, as a low word that address steps are added to and a constant
+// high word: an MMA of 64 cycles must not wait for its descriptor arithmetic (formed anew
+// for each, a 128 x 128 x 128 product took 730 to 830 cycles instead of 516).
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+// K-major (Q, K): rows of 128 bytes.
+__device__ __forceinline__ uint32_t desc_k(const void* p) { return smem_u32(p) >> 4 | 1u << 16; }
+// N-major (V, whose tokens are the product's K): 64-element column blocks kHalfBytes apart.
+__device__ __forceinline__ uint32_t desc_n(const void* p) { return smem_u32(p) >> 4 | (kHalfBytes >> 4) << 16; }
+// Step of a K-major descriptor to elements 16 kk .., of an N-major one to tokens 16 kk ..
+__device__ __forceinline__ constexpr uint32_t step_k(int kk) {
+  return ((kk >> 2) * kHalfBytes + static_cast<uint32_t>(kk & 3) * 32) >> 4;
 }
-// N-major (V: tokens are K): 64-element column blocks kHalfBytes apart, 8-token groups 1024
-// bytes apart.
-__device__ __forceinline__ uint64_t desc_n(uint32_t addr) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(kHalfBytes >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+__device__ __forceinline__ constexpr uint32_t step_n(int kk) { return static_cast<uint32_t>(kk) * 2048 >> 4; }
 // fp32 accumulate, bf16 or f16 operands, M = N = 128; B N-major for the value product.
 template <bool F16>
 __device__ __forceinline__ constexpr uint32_t idesc(bool b_n_major) {
   return (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (b_n_major ? 1u << 16 : 0u) | ((128u >> 3) << 17) |
          ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
+      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(static_cast<uint32_t>(acc)), "n"(kDescHi), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-          d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %6, 0;\n"
+      " mov.b64 b, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(static_cast<uint32_t>(acc)), "n"(kDescHi), "r"(one)
       : "memory");
 }
 
@@ -305,72 +320,97 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
   __syncwarp();
 }
 
-// ------------------------------------------------------------------ MMAs (one thread)
+// ------------------------------------------------------------------ MMAs (one warp)
+// Place in the ring of K and V tiles.
+struct Place {
+  int st = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ Place next() const {
+    Place p;
+    p.st = st + 1 == kStages ? 0 : st + 1;
+    p.phase = st + 1 == kStages ? phase ^ 1 : phase;
+    return p;
+  }
+};
+
 template <bool F16>
 __device__ void mma_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
   volatile int* dead = &s.dead;
-  int it = 0, n_q = 0, n_p[2] = {0, 0};
+  const uint32_t one = elect_one();
+  uint32_t q_phase = 0, p_phase[2] = {0, 0};
+  const uint32_t q0 = desc_k(s.q[0]), k0 = desc_k(s.kv[0]), v0 = desc_n(s.kv[0]);
+  auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait_phase(bar, phase, dead)); };
   auto scores = [&](int x, int st) {
-    const uint32_t q = smem_u32(s.q[x]), k = smem_u32(s.kv[st]);
+    const uint32_t d = tmem + x * 128, q = q0 + x * (kTileBytes >> 4), k = k0 + st * (kTileBytes >> 4);
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;  // 16 elements = 32 bytes
-      mma_ss(tmem + x * 128, desc_k(q + off), desc_k(k + off), idesc<F16>(false), kk > 0);
-    }
-    tc_commit(&s.s_full[x]);
+    for (int kk = 0; kk < 8; ++kk) mma_ss(d, q + step_k(kk), k + step_k(kk), idesc<F16>(false), kk > 0, one);
+    tc_commit(&s.s_full[x], one);
   };
+  auto values = [&](int x, int st, bool acc, int groups) {
+    const uint32_t d = tmem + 256 + x * 128, p = tmem + x * 128, v = v0 + st * (kTileBytes >> 4);
+    mma_ts(d, p, v, idesc<F16>(true), acc, one);
+    if (groups == 8) {
+#pragma unroll
+      for (int g = 1; g < 8; ++g) mma_ts(d, p + 8 * g, v + step_n(g), idesc<F16>(true), true, one);
+    } else {
+      for (int g = 1; g < groups; ++g) mma_ts(d, p + 8 * g, v + step_n(g), idesc<F16>(true), true, one);
+    }
+  };
+  Place k;  // the next K tile
   bool ok = true;
   for (int n = 0;; ++n) {
-    if (!(ok = wait_phase(&s.part_full[n & 1], (n >> 1) & 1, dead))) break;
-    const Part d = s.part[n & 1];
-    mbar_arrive(&s.part_empty[n & 1]);
-    if (d.steps > 0) {
-      if (!(ok = wait_phase(&s.q_full, n_q & 1, dead))) break;
-      ++n_q;
-      if (!(ok = wait_phase(&s.kv_full[it % kStages], (it / kStages) & 1, dead))) break;
+    if (!(ok = wait(&s.part_full[n & 1], (n >> 1) & 1))) break;
+    const int steps = s.part[n & 1].steps, tail = s.part[n & 1].tail, last = s.part[n & 1].last;
+    const int two = s.part[n & 1].two, end = s.part[n & 1].end;
+    __syncwarp();
+    if (one) mbar_arrive(&s.part_empty[n & 1]);
+    if (steps > 0) {
+      if (!(ok = wait(&s.q_full, q_phase))) break;
+      q_phase ^= 1;
+      if (!(ok = wait(&s.kv_full[k.st], k.phase))) break;
       tc_fence_after();
-      for (int x = 0; x <= d.two; ++x) scores(x, it % kStages);
-      tc_commit(&s.kv_empty[it % kStages]);
-      if (d.steps == 1) tc_commit(&s.q_empty);
+      scores(0, k.st);
+      if (two) scores(1, k.st);
+      tc_commit(&s.kv_empty[k.st], one);
+      if (steps == 1) tc_commit(&s.q_empty, one);
     }
-    for (int j = 0; j < d.steps && ok; ++j, it += 2) {
-      const int vs = (it + 1) % kStages, ks = (it + 2) % kStages;
-      const bool more = j + 1 < d.steps;
-      if (!(ok = wait_phase(&s.kv_full[vs], ((it + 1) / kStages) & 1, dead))) break;
+    for (int j = 0; j < steps; ++j) {
+      const Place v = k.next();
+      k = v.next();
+      const bool more = j + 1 < steps;
       // tokens past the end add nothing: only their groups of 16 that hold a token
-      const int groups = d.last && !more ? (d.tail + 15) >> 4 : 8;
-      for (int x = 0; x <= d.two && ok; ++x) {
-        if (!(ok = wait_phase(&s.p_full[x], n_p[x]++ & 1, dead))) break;
+      const int groups = last && !more ? (tail + 15) >> 4 : 8;
+      if (!(ok = wait(&s.kv_full[v.st], v.phase))) break;
+      if (more && !(ok = wait(&s.kv_full[k.st], k.phase))) break;
+      if (!(ok = wait(&s.p_full[0], p_phase[0]))) break;
+      p_phase[0] ^= 1;
+      tc_fence_after();
+      values(0, v.st, j > 0, groups);
+      if (!more) tc_commit(&s.o_full[0], one);
+      if (more) scores(0, k.st);
+      if (two) {
+        if (!(ok = wait(&s.p_full[1], p_phase[1]))) break;
+        p_phase[1] ^= 1;
         tc_fence_after();
-        const uint32_t v = smem_u32(s.kv[vs]);
-        for (int g = 0; g < groups; ++g)
-          mma_ts(tmem + 256 + x * 128, tmem + x * 128 + 8 * g, desc_n(v + g * 2048), idesc<F16>(true), j > 0 || g > 0);
-        if (x == d.two) tc_commit(&s.kv_empty[vs]);
-        if (!more) {
-          tc_commit(&s.o_full[x]);
-        } else {
-          if (x == 0) {
-            if (!(ok = wait_phase(&s.kv_full[ks], ((it + 2) / kStages) & 1, dead))) break;
-            tc_fence_after();
-          }
-          scores(x, ks);
-          if (x == d.two) {
-            tc_commit(&s.kv_empty[ks]);
-            if (j + 2 == d.steps) tc_commit(&s.q_empty);
-          }
-        }
+        values(1, v.st, j > 0, groups);
+        if (!more) tc_commit(&s.o_full[1], one);
+        if (more) scores(1, k.st);
       }
+      tc_commit(&s.kv_empty[v.st], one);
+      if (more) tc_commit(&s.kv_empty[k.st], one);
+      if (j + 2 == steps) tc_commit(&s.q_empty, one);
     }
-    if (!ok || d.end) break;
+    if (!ok || end) break;
   }
-  if (!ok) {
+  if (!ok && one) {
     *dead = 1;
     if (a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_TIMEOUT));
   }
   // the MMAs issued complete before TMEM is freed (bounded)
   volatile int never = 0;
-  tc_commit(&s.drain);
+  tc_commit(&s.drain, one);
   (void)wait_phase(&s.drain, 0, &never);
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ rows (four warps a tile)
@@ -601,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CrossArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.kv_full[i], 1);
@@ -689,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) load_role(a, s, &kv_map, &q_map, f0, f1, n_cta);
-    if (warp == kMmaWarp && lane == 0) mma_role<F16>(a, s, tmem);
+    if (warp == kMmaWarp) mma_role<F16>(a, s, tmem);
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRowRegs));
