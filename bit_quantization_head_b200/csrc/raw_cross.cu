@@ -41,43 +41,52 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr uint32_t kHalfBytes = 128 * 128;       // 64 elements of 128 rows
 constexpr uint32_t kTileBytes = 2 * kHalfBytes;
-constexpr int kStages = 5;                       // K or V tiles in flight
+constexpr int kStages = 4;                       // K or V tiles in flight (a power of 2)
 constexpr int kMaxCtas = 160;                    // partial slots in the workspace
 constexpr int kPartFloats = kRows * (kD + 2);    // (m, l) of each row, then its sums
 constexpr uint32_t kTmemCols = 512;              // S_a, S_b, O_a, O_b
 // Registers of a thread: 384 threads start with 168 each (64512); the row warps take what
 // the others leave (2 * 216 + 72 = 3 * 168).
 constexpr int kRowRegs = 216, kOtherRegs = 72;
+// Steps of a unit of one tile from which the second tile takes every other one.
+constexpr int kTwinSteps = 4;
+// Pairs of eight whose weights are formed on the FMA pipe.
+constexpr uint32_t kFmaExp = 0x92;
 constexpr float kSlack = 8.0f;                   // log2 of what p may reach before m moves
 
 // The part of a unit that this CTA computes.
 struct Part {
   int steps;        // 128-token steps (0: no tokens or a bad page)
-  int tail;         // tokens of the last step
+  int tail;         // tokens of the unit's last step
   int tok0, tok1;   // query tokens of the unit
   int head;         // KV head
-  int two;          // whether the second tile has rows
+  int two;          // whether the second tile has rows of its own
+  int twin;         // whether it takes every other step of the first one's
   int first, last;  // whether the part holds the unit's first and last step
   int bad;
   int c0, c1;       // CTAs that share the unit
   int end;          // last part of the run
 };
 
+// A sequence as the kernel uses it: its query rows, tokens, units per KV head and steps.
+struct Seq {
+  int tok0, tok1, len, blocks, steps;
+  bool bad;
+};
+
 struct __align__(1024) Smem {
   unsigned char q[2][kTileBytes];
   unsigned char kv[kStages][kTileBytes];
+  unsigned char out[8][32 * 128];  // half of each row warp's output rows
   Part part[2];
   uint64_t kv_full[kStages], kv_empty[kStages], q_full, q_empty, part_full[2], part_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], join[2], drain;
-  long long warp_sum[kWarps];
-  int warp_max[kWarps];
-  long long first_step, total;
-  int first_seq;
+  uint64_t s_full[2], p_full[2][2], o_full[2], join[2], twin_full, twin_empty, drain;
   int dead;
-  int last_in[2];
+  int arrived[2][2];       // [tile][part & 1]
+  float2 twin_ml[kRows];   // the second tile's m and l of a twin part
   uint32_t tmem;
 };
-
+static_assert((kStages & (kStages - 1)) == 0, "places in the ring are taken modulo kStages");
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory of a CTA");
 
 struct CrossArgs {
@@ -137,6 +146,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// -inf into N columns (1 or 8) of this warp's lanes.
+template <int N>
+__device__ __forceinline__ void tmem_fill(uint32_t taddr) {
+  if (N == 1)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(0xFF800000u) : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};\n" ::"r"(taddr),
+                 "r"(0xFF800000u)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 // Shared-memory matrix descriptors, 128-byte swizzle (layout type 2, version 1), 8-row
@@ -194,17 +213,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
-// A sequence as the kernel uses it: its query rows, tokens, units per KV head and steps.
-struct Seq {
-  int tok0, tok1, len, blocks, steps;
-  bool bad;
-};
 __device__ __forceinline__ Seq seq_of(const CrossArgs& a, int s) {
   Seq q;
   q.tok0 = a.cu_q[s];
@@ -222,18 +241,97 @@ __device__ __forceinline__ Seq seq_of(const CrossArgs& a, int s) {
   return q;
 }
 
+// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer, 2^f by a polynomial
+// (minimax in relative error on [-1/2, 1/2], fitted for this kernel: 2^-13.7 for bf16
+// weights, 2^-18.5 for fp16), times 2^n.  x is held above -126; NaN stays NaN.
+template <bool F16>
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
+  float a, b;
+  unpair(x, a, b);
+  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(a) : "f"(-126.0f));
+  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(b) : "f"(-126.0f));
+  x = pair(a, b);
+  const uint64_t t = add2(x, pair(12582912.0f, 12582912.0f));  // 1.5 * 2^23 + n
+  const uint64_t n = add2(t, pair(-12582912.0f, -12582912.0f));
+  const uint64_t f = fma2(n, pair(-1.0f, -1.0f), x);
+  uint64_t p;
+  if (F16) {
+    p = fma2(f, pair(0.00957010221f, 0.00957010221f), pair(0.0559178591f, 0.0559178591f));
+    p = fma2(f, p, pair(0.240247443f, 0.240247443f));
+    p = fma2(f, p, pair(0.693121791f, 0.693121791f));
+    p = fma2(f, p, pair(0.999999285f, 0.999999285f));
+  } else {
+    p = fma2(f, pair(0.0551716685f, 0.0551716685f), pair(0.242611125f, 0.242611125f));
+    p = fma2(f, p, pair(0.693260968f, 0.693260968f));
+    p = fma2(f, p, pair(0.999928057f, 0.999928057f));
+  }
+  unpair(t, a, b);
+  a = __uint_as_float((__float_as_uint(a) << 23) + 0x3F800000u);
+  b = __uint_as_float((__float_as_uint(b) << 23) + 0x3F800000u);
+  return mul2(p, pair(a, b));
+}
+
 // ------------------------------------------------------------------ loads (one warp)
-__device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map, const CUtensorMap* q_map,
-                          long long f, long long f1, int n_cta) {
+__device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map, const CUtensorMap* q_map) {
   const int lane = threadIdx.x & 31;
   volatile int* dead = &s.dead;
-  int seq = s.first_seq, n_part = 0, n_q = 0, it = 0;
-  long long base = s.first_step;  // first step of the sequence's units
-  Seq sq = seq_of(a, seq);
+  // steps of all sequences and the longest one
+  long long total = 0;
+  int longest = 0;
+  bool bad_seq = false;
+  Seq sq;
+  for (int i = lane; i < a.n_seq; i += 32) {
+    sq = seq_of(a, i);
+    bad_seq |= sq.bad;
+    total += static_cast<long long>(sq.steps) * sq.blocks;
+    if (sq.blocks) longest = max(longest, sq.steps);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  total *= a.H;
+  if (bad_seq && blockIdx.x == 0 && a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_BAD_POS));
+  // A run of r steps saves (longest / r) joins of about half a step each at the end of a
+  // unit: no run shorter than sqrt(longest / 2).
+  const int shortest = max(1, static_cast<int>(sqrtf(0.5f * static_cast<float>(longest))));
+  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), divide(total + shortest - 1, shortest)));
+  long long f = 0, f1 = 0;
+  if (static_cast<int>(blockIdx.x) < n_cta) {
+    f = run_start(blockIdx.x, n_cta, total);
+    f1 = run_start(blockIdx.x + 1, n_cta, total);
+  } else if (lane == 0) {  // nothing for this CTA
+    Part d = {};
+    d.first = d.last = d.end = 1;
+    s.part[0] = d;
+    mbar_arrive(&s.part_full[0]);
+  }
+  // the sequence of the run's first step
+  int seq = 0, n_part = 0, n_q = 0, it = 0;
+  long long base = 0;  // first step of the sequence's units
+  for (int i0 = 0; f < f1; i0 += 32) {
+    const int i = i0 + lane;
+    if (a.n_seq > 32) sq = seq_of(a, min(i, a.n_seq - 1));
+    const long long mine = i < a.n_seq ? static_cast<long long>(sq.steps) * sq.blocks * a.H : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, f < base + incl);  // lanes at or past it
+    if (past) {
+      const int at = __ffs(past) - 1;
+      seq = i0 + at;
+      base += __shfl_sync(0xffffffffu, incl - mine, at);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  sq = seq_of(a, seq);
   uint32_t flags = 0;
   bool ok = true;
   auto load = [&](int row) {  // the 128 rows from `row` into the next stage (lane 0)
-    const int st = it % kStages;
+    const int st = it & (kStages - 1);
     if (it >= kStages && !wait_phase(&s.kv_empty[st], (it / kStages - 1) & 1, dead)) return false;
     mbar_arrive_expect_tx(&s.kv_full[st], kTileBytes);
     tma_load_2d(s.kv[st], kv_map, 0, row, &s.kv_full[st]);
@@ -246,17 +344,23 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
       base += static_cast<long long>(sq.steps) * a.H * sq.blocks;
       sq = seq_of(a, ++seq);
     }
-    const int u = static_cast<int>((f - base) / sq.steps), h = u / sq.blocks, blk = u - h * sq.blocks;
+    const int u = static_cast<int>(divide(f - base, sq.steps)), h = u / sq.blocks, blk = u - h * sq.blocks;
     const long long begin = base + static_cast<long long>(u) * sq.steps;
     const int i0 = static_cast<int>(f - begin);
     const int i1 = static_cast<int>(min(static_cast<long long>(sq.steps), i0 + (f1 - f)));
     const int32_t* pages = a.table + static_cast<size_t>(seq) * a.max_pages;
     bool good = true;
-    if (sq.len > 0)
-      for (int p = i0 + lane; p < i1; p += 32) {
+    int ids = 0;  // the next 32 page ids, one per lane
+    if (sq.len > 0) {
+      for (int p = i0 + 32 + lane; p < i1; p += 32) {
         const int id = pages[p];
         good &= id >= 0 && id < a.n_pages;
       }
+      if (i0 + lane < i1) {
+        ids = pages[i0 + lane];
+        good &= ids >= 0 && ids < a.n_pages;
+      }
+    }
     good = __all_sync(0xffffffffu, good);
     if (!good) flags |= KVTC_STATUS_BAD_PAGE;
     const int steps = good && sq.len > 0 ? i1 - i0 : 0;
@@ -267,11 +371,12 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
     d.tok1 = min(sq.tok1, d.tok0 + 2 * a.tile_tok);
     d.head = h;
     d.two = d.tok1 - d.tok0 > a.tile_tok;
+    d.twin = !d.two && sq.steps >= kTwinSteps;
     d.first = i0 == 0;
     d.last = i1 == sq.steps;
     d.bad = !good;
-    d.c0 = run_owner(begin, n_cta, s.total);
-    d.c1 = run_owner(begin + sq.steps - 1, n_cta, s.total);
+    d.c0 = run_owner(begin, n_cta, total);
+    d.c1 = run_owner(begin + sq.steps - 1, n_cta, total);
     f += i1 - i0;
     d.end = f >= f1;
     if (lane == 0) {
@@ -282,9 +387,8 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
       }
     }
     ++n_part;
-    int ids = 0;
     for (int i = i0; i < i0 + steps; ++i) {
-      if (((i - i0) & 31) == 0) ids = i + lane < i1 ? pages[i + lane] : 0;
+      if (i > i0 && ((i - i0) & 31) == 0) ids = i + lane < i1 ? pages[i + lane] : 0;
       const int id = __shfl_sync(0xffffffffu, ids, (i - i0) & 31);
       if (lane == 0 && ok) {
         const int row = a.row0 + (id * a.H + h) * 2 * kPage;
@@ -314,92 +418,117 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
     if (flags && a.status) atomicOr(a.status, static_cast<int>(flags));
     // every copy in flight lands before the CTA may exit (bounded)
     volatile int never = 0;
-    for (int k = max(0, it - kStages); k < it; ++k) (void)wait_phase(&s.kv_full[k % kStages], (k / kStages) & 1, &never);
+    for (int k = max(0, it - kStages); k < it; ++k) (void)wait_phase(&s.kv_full[k & (kStages - 1)], (k / kStages) & 1, &never);
     if (n_q > 0) (void)wait_phase(&s.q_full, (n_q - 1) & 1, &never);
   }
   __syncwarp();
 }
 
 // ------------------------------------------------------------------ MMAs (one warp)
-// Place in the ring of K and V tiles.
-struct Place {
-  int st = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ Place next() const {
-    Place p;
-    p.st = st + 1 == kStages ? 0 : st + 1;
-    p.phase = st + 1 == kStages ? phase ^ 1 : phase;
-    return p;
-  }
-};
-
 template <bool F16>
 __device__ void mma_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
   volatile int* dead = &s.dead;
   const uint32_t one = elect_one();
   uint32_t q_phase = 0, p_phase[2] = {0, 0};
   const uint32_t q0 = desc_k(s.q[0]), k0 = desc_k(s.kv[0]), v0 = desc_n(s.kv[0]);
-  auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait_phase(bar, phase, dead)); };
-  auto scores = [&](int x, int st) {
-    const uint32_t d = tmem + x * 128, q = q0 + x * (kTileBytes >> 4), k = k0 + st * (kTileBytes >> 4);
+  auto wait = [&](uint64_t* bar, uint32_t phase) { return wait_warp(bar, phase, dead); };
+  // waits for tile i of the ring, and releases it
+  auto loaded = [&](int i) { return wait(&s.kv_full[i & (kStages - 1)], (i / kStages) & 1); };
+  auto release = [&](int i) { tc_commit(&s.kv_empty[i & (kStages - 1)], one); };
+  auto scores = [&](int x, int rows, int i) {  // S_x of the rows of Q tile `rows`
+    const uint32_t d = tmem + x * 128, q = q0 + rows * (kTileBytes >> 4);
+    const uint32_t k = k0 + (i & (kStages - 1)) * (kTileBytes >> 4);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) mma_ss(d, q + step_k(kk), k + step_k(kk), idesc<F16>(false), kk > 0, one);
     tc_commit(&s.s_full[x], one);
   };
-  auto values = [&](int x, int st, bool acc, int groups) {
-    const uint32_t d = tmem + 256 + x * 128, p = tmem + x * 128, v = v0 + st * (kTileBytes >> 4);
-    mma_ts(d, p, v, idesc<F16>(true), acc, one);
+  // O_x += P_x V for the first `groups` groups of 16 tokens, each half of P as it arrives
+  auto values = [&](int x, int i, bool acc, int groups) -> bool {
+    const uint32_t d = tmem + 256 + x * 128, p = tmem + x * 128, v = v0 + (i & (kStages - 1)) * (kTileBytes >> 4);
+    if (!wait(&s.p_full[x][0], p_phase[x])) return false;
+    tc_fence_after();
     if (groups == 8) {
 #pragma unroll
-      for (int g = 1; g < 8; ++g) mma_ts(d, p + 8 * g, v + step_n(g), idesc<F16>(true), true, one);
+      for (int g = 0; g < 4; ++g) mma_ts(d, p + 8 * g, v + step_n(g), idesc<F16>(true), acc || g > 0, one);
+      if (!wait(&s.p_full[x][1], p_phase[x])) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int g = 4; g < 8; ++g) mma_ts(d, p + 8 * g, v + step_n(g), idesc<F16>(true), true, one);
     } else {
-      for (int g = 1; g < groups; ++g) mma_ts(d, p + 8 * g, v + step_n(g), idesc<F16>(true), true, one);
+      if (!wait(&s.p_full[x][1], p_phase[x])) return false;
+      tc_fence_after();
+      for (int g = 0; g < groups; ++g) mma_ts(d, p + 8 * g, v + step_n(g), idesc<F16>(true), acc || g > 0, one);
     }
+    p_phase[x] ^= 1;
+    return true;
   };
-  Place k;  // the next K tile
+  int it = 0;  // the part's first K tile in the ring; V of step j is it + 2 j + 1
   bool ok = true;
   for (int n = 0;; ++n) {
     if (!(ok = wait(&s.part_full[n & 1], (n >> 1) & 1))) break;
-    const int steps = s.part[n & 1].steps, tail = s.part[n & 1].tail, last = s.part[n & 1].last;
-    const int two = s.part[n & 1].two, end = s.part[n & 1].end;
+    const Part& d = s.part[n & 1];
+    const int steps = d.steps, two = d.two, twin = d.twin, end = d.end;
+    // tokens past the end add nothing: only the last step's groups of 16 that hold a token
+    const int last_groups = d.last ? (d.tail + 15) >> 4 : 8;
     __syncwarp();
     if (one) mbar_arrive(&s.part_empty[n & 1]);
     if (steps > 0) {
       if (!(ok = wait(&s.q_full, q_phase))) break;
       q_phase ^= 1;
-      if (!(ok = wait(&s.kv_full[k.st], k.phase))) break;
+      if (!(ok = loaded(it))) break;
       tc_fence_after();
-      scores(0, k.st);
-      if (two) scores(1, k.st);
-      tc_commit(&s.kv_empty[k.st], one);
-      if (steps == 1) tc_commit(&s.q_empty, one);
-    }
-    for (int j = 0; j < steps; ++j) {
-      const Place v = k.next();
-      k = v.next();
-      const bool more = j + 1 < steps;
-      // tokens past the end add nothing: only their groups of 16 that hold a token
-      const int groups = last && !more ? (tail + 15) >> 4 : 8;
-      if (!(ok = wait(&s.kv_full[v.st], v.phase))) break;
-      if (more && !(ok = wait(&s.kv_full[k.st], k.phase))) break;
-      if (!(ok = wait(&s.p_full[0], p_phase[0]))) break;
-      p_phase[0] ^= 1;
-      tc_fence_after();
-      values(0, v.st, j > 0, groups);
-      if (!more) tc_commit(&s.o_full[0], one);
-      if (more) scores(0, k.st);
-      if (two) {
-        if (!(ok = wait(&s.p_full[1], p_phase[1]))) break;
-        p_phase[1] ^= 1;
+      scores(0, 0, it);
+      if (two) scores(1, 1, it);
+      release(it);
+      if (twin && steps > 1) {
+        if (!(ok = loaded(it + 2))) break;
         tc_fence_after();
-        values(1, v.st, j > 0, groups);
-        if (!more) tc_commit(&s.o_full[1], one);
-        if (more) scores(1, k.st);
+        scores(1, 0, it + 2);
+        release(it + 2);
       }
-      tc_commit(&s.kv_empty[v.st], one);
-      if (more) tc_commit(&s.kv_empty[k.st], one);
-      if (j + 2 == steps) tc_commit(&s.q_empty, one);
+      if (steps <= 1 + twin) tc_commit(&s.q_empty, one);
     }
+    if (!twin) {
+      for (int j = 0; j < steps; ++j) {
+        const int v = it + 2 * j + 1, k = v + 1;
+        const bool more = j + 1 < steps;
+        const int groups = more ? 8 : last_groups;
+        if (!(ok = loaded(v) && values(0, v, j > 0, groups))) break;
+        if (more) {
+          if (!(ok = loaded(k))) break;
+          tc_fence_after();
+          scores(0, 0, k);
+        } else {
+          tc_commit(&s.o_full[0], one);
+        }
+        if (two) {
+          if (!(ok = values(1, v, j > 0, groups))) break;
+          if (more)
+            scores(1, 1, k);
+          else
+            tc_commit(&s.o_full[1], one);
+        }
+        release(v);
+        if (more) release(k);
+        if (j + 2 == steps) tc_commit(&s.q_empty, one);
+      }
+    } else {
+      for (int j = 0; j < steps; ++j) {
+        const int x = j & 1, v = it + 2 * j + 1, k = v + 3;
+        if (!(ok = loaded(v) && values(x, v, j > 1, j + 1 < steps ? 8 : last_groups))) break;
+        release(v);
+        if (j + 2 < steps) {
+          if (!(ok = loaded(k))) break;
+          tc_fence_after();
+          scores(x, 0, k);
+          release(k);
+          if (j + 3 == steps) tc_commit(&s.q_empty, one);
+        } else {
+          tc_commit(&s.o_full[x], one);
+        }
+      }
+    }
+    it += 2 * steps;
     if (!ok || end) break;
   }
   if (!ok && one) {
@@ -432,17 +561,14 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
   const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
   const int tok_in = row / a.G, head_in = row - tok_in * a.G;
   const uint64_t c2 = pair(a.c, a.c);
-  uint32_t join_phase = 0;
+  uint32_t join_phase = 0, twin_phase = 0;
   int it = 0, n_s = 0, n_o = 0;
-  auto give_up = [&] {
-    if (lane == 0) {
+  auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
+    const bool ok = wait_warp(bar, phase, dead);
+    if (!ok && lane == 0) {
       *dead = 1;
       if (a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_TIMEOUT));
     }
-  };
-  auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
-    const bool ok = __all_sync(0xffffffffu, wait_phase(bar, phase, dead));
-    if (!ok) give_up();
     return ok;
   };
   // Barrier of the tile's four warps.
@@ -457,52 +583,60 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
     const Part d = s.part[n & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.part_empty[n & 1]);
-    if (x == 0 || d.two) {
+    if (x == 0 || d.two || d.twin) {
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < d.steps; ++j) {
-        const int valid = d.last && j == d.steps - 1 ? d.tail : kPage;
+      const int stride = 1 + d.twin, t0 = d.twin ? x : 0;
+      const bool some = t0 < d.steps;  // the tile has steps
+      for (int t = t0; t < d.steps; t += stride) {
+        const int valid = d.last && t == d.steps - 1 ? d.tail : kPage;
         if (!wait(&s.s_full[x], n_s++ & 1)) return;
         tc_fence_after();
-        float sc[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, sc + 32 * i);
-        tmem_wait_ld();
         if (valid < kPage) {
+          // scores past the end, in TMEM: the code of a full step then serves the last one
+          int i = valid;
+          for (; i & 7; ++i) tmem_fill<1>(ts + i);
+          for (; i < kPage; i += 8) tmem_fill<8>(ts + i);
+          tmem_wait_st();
+        }
+        float top;
+        {
+          float sc[128];
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= valid) sc[i] = -INFINITY;
-          if (x == 0 && (valid & 15)) {
-            // V rows past the end may hold anything (0 * NaN is NaN): clear those that the
-            // last group of 16 tokens takes in
-            const int vi = it + 2 * j + 1, st = vi % kStages;
-            if (!wait(&s.kv_full[st], (vi / kStages) & 1)) return;
-            for (int e = row; e < (16 - (valid & 15)) * 16; e += 128) {
-              const int r = valid + (e >> 4);
-              *reinterpret_cast<uint4*>(s.kv[st] + ((e >> 3) & 1) * kHalfBytes + r * 128 + (e & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
+          for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, sc + 32 * i);
+          tmem_wait_ld();
+          float m0 = sc[0], m1 = sc[1], m2 = sc[2], m3 = sc[3];
+#pragma unroll
+          for (int i = 4; i < 124; i += 8) {
+            m0 = max3(m0, sc[i], sc[i + 1]);
+            m1 = max3(m1, sc[i + 2], sc[i + 3]);
+            m2 = max3(m2, sc[i + 4], sc[i + 5]);
+            m3 = max3(m3, sc[i + 6], sc[i + 7]);
           }
+          m0 = max3(m0, sc[124], sc[125]);
+          m1 = max3(m1, sc[126], sc[127]);
+          top = fmaxf(max3(m0, m1, m2), m3);
         }
-        float t0 = sc[0], t1 = sc[1], t2 = sc[2], t3 = sc[3];
-#pragma unroll
-        for (int i = 4; i < 124; i += 8) {
-          t0 = max3(t0, sc[i], sc[i + 1]);
-          t1 = max3(t1, sc[i + 2], sc[i + 3]);
-          t2 = max3(t2, sc[i + 4], sc[i + 5]);
-          t3 = max3(t3, sc[i + 6], sc[i + 7]);
+        if (valid < kPage && (x == 0 || d.twin) && (valid & 15)) {
+          // V rows past the end may hold anything (0 * NaN is NaN): clear those that the
+          // last group of 16 tokens takes in
+          const int v = it + 2 * t + 1, st = v & (kStages - 1);
+          if (!wait(&s.kv_full[st], (v / kStages) & 1)) return;
+          for (int e = row; e < (16 - (valid & 15)) * 16; e += 128) {
+            const int r = valid + (e >> 4);
+            *reinterpret_cast<uint4*>(s.kv[st] + ((e >> 3) & 1) * kHalfBytes + r * 128 + (e & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
         }
-        t0 = max3(t0, sc[124], sc[125]);
-        t1 = max3(t1, sc[126], sc[127]);
-        const float top = fmaxf(max3(t0, t1, t2), t3);
         if (__any_sync(0xffffffffu, (top - m) * a.c > kSlack)) {
           const float to_m = fmaxf(m, top);
           const float f = m == -INFINITY ? 0.0f : ex2((m - to_m) * a.c);
           l *= f;
           m = to_m;
-          if (j > 0) {
-            // S(j) was issued after PV(j - 1), so the accumulators are complete
-#pragma unroll
+          if (t > t0) {
+            // these scores were issued after the tile's last value product, so the
+            // accumulators are complete
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               float o[32];
               uint32_t w[32];
@@ -517,117 +651,220 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
         const float neg = kBias - m * a.c;
         const uint64_t neg2 = pair(neg, neg);
         uint64_t sum0 = pair(0.0f, 0.0f), sum1 = sum0;
-#pragma unroll
+        // The scores are read from TMEM once more, 64 columns at a time in one piece of code:
+        // with 128 in registers the unrolled loop outgrew the instruction caches (half as
+        // many stalls for instructions as instructions issued), the MMA warp's with it.  P
+        // takes the columns of scores that have been read.
+#pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
+          float sc[64];
           uint32_t w[32];
+          tmem_ld32(ts + 64 * hf, sc);
+          tmem_ld32(ts + 64 * hf + 32, sc + 32);
+          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int e = 64 * hf + 2 * i;
+            const int e = 2 * i;
+            uint64_t p = fma2(pair(sc[e], sc[e + 1]), c2, neg2);
             float lo, hi;
-            unpair(fma2(pair(sc[e], sc[e + 1]), c2, neg2), lo, hi);
-            lo = ex2(lo);
-            hi = ex2(hi);
+            if (kFmaExp >> (i & 7) & 1) {
+              p = exp2_pair<F16>(p);
+              unpair(p, lo, hi);
+            } else {
+              unpair(p, lo, hi);
+              lo = ex2(lo);
+              hi = ex2(hi);
+              p = pair(lo, hi);
+            }
             if (i & 1)
-              sum1 = add2(sum1, pair(lo, hi));
+              sum1 = add2(sum1, p);
             else
-              sum0 = add2(sum0, pair(lo, hi));
+              sum0 = add2(sum0, p);
             // P enters the value product in the pages' type (half a step of relative error
             // on each weight, as for the output; the sum l stays fp32)
             w[i] = pack2<F16>(lo, hi);
           }
           tmem_st32(ts + 32 * hf, w);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.p_full[x][hf]);
         }
         float a0, a1;
         unpair(add2(sum0, sum1), a0, a1);
         l += a0 + a1;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.p_full[x]);
       }
-      if (d.steps > 0) {
+      // ---- the tile's steps are done
+      const bool whole = d.first && d.last;
+      const int shares = d.c1 - d.c0 + 1;
+      int* ticket = a.tickets + 2 * d.c0 + x;
+      if (!whole && row == 0) s.arrived[x][n & 1] = ld_acquire_gpu(ticket);
+      if (some) {
         if (!wait(&s.o_full[x], n_o++ & 1)) return;
         tc_fence_after();
       }
-      const int tok = d.tok0 + x * a.tile_tok + tok_in;
-      const bool live = tok_in < a.tile_tok && tok < d.tok1;
-      uint16_t* dst = a.out + (static_cast<size_t>(tok) * a.H * a.G + static_cast<size_t>(d.head) * a.G + head_in) * kD;
-      const bool whole = d.first && d.last;
-      float* mine = part_of(a, blockIdx.x, d.first, x);
-      const float r = whole && d.steps > 0 ? 1.0f / l : 0.0f;
-      if (!whole && live) reinterpret_cast<float2*>(mine)[row] = make_float2(m, d.bad ? -1.0f : l);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float o[32];
+      // a twin part: the first tile's warps take the second's sums (the same rows, so the
+      // same TMEM lanes) in with their own
+      float fa = 1.0f, fb = 0.0f;
+      if (d.twin && x == 1) {
+        s.twin_ml[row] = make_float2(m, l);
+        tc_fence_before();
         __syncwarp();
-        if (d.steps > 0) {
-          tmem_ld32(to + 32 * i, o);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-        }
-        if (!live) continue;
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = pack2<F16>(o[e] * r, o[e + 1] * r);
-            w.y = pack2<F16>(o[e + 2] * r, o[e + 3] * r);
-            w.z = pack2<F16>(o[e + 4] * r, o[e + 5] * r);
-            w.w = pack2<F16>(o[e + 6] * r, o[e + 7] * r);
-            reinterpret_cast<uint4*>(dst + 32 * i + e)[0] = w;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            reinterpret_cast<float4*>(mine + 2 * kRows)[(8 * i + e / 4) * kRows + row] =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        if (lane == 0) mbar_arrive(&s.twin_full);
+        if (!wait(&s.twin_empty, twin_phase)) return;
+        twin_phase ^= 1;
+        tc_fence_after();
+        it += 2 * d.steps;
+        if (d.end) return;
+        continue;
+      }
+      const bool both = d.twin && d.steps > 1;
+      if (d.twin) {
+        if (!wait(&s.twin_full, twin_phase)) return;
+        twin_phase ^= 1;
+        tc_fence_after();
+        if (both) {
+          const float2 ml = s.twin_ml[row];
+          const float to_m = fmaxf(m, ml.x);
+          fa = ex2((m - to_m) * a.c);
+          fb = ex2((ml.x - to_m) * a.c);
+          m = to_m;
+          l = l * fa + ml.y * fb;
         }
       }
-      if (!whole) {
-        // ---- the unit is shared with other CTAs: the last one to arrive joins the parts
-        __threadfence();
-        if (!tile_sync()) return;
-        if (row == 0) s.last_in[x] = atomicAdd(a.tickets + 2 * d.c0 + x, 1) == d.c1 - d.c0;
-        if (!tile_sync()) return;
-        if (s.last_in[x]) {
-          __threadfence();
-          if (row == 0) a.tickets[2 * d.c0 + x] = 0;
-          if (live) {
-            float top = -INFINITY;
-            bool bad = false;
-            for (int c = d.c0; c <= d.c1; ++c) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(a, c, c == d.c0, x)) + row);
-              top = fmaxf(top, ml.x);
-              bad |= ml.y < 0.0f;
-            }
-            float sum = 0.0f, o[128];
+      const int tok = d.tok0 + x * a.tile_tok + tok_in;
+      const bool live = tok_in < a.tile_tok && tok < d.tok1;
+      // offset of the lane's output row, -1 without one
+      const long long at = live ? (static_cast<long long>(tok) * a.H * a.G + static_cast<long long>(d.head) * a.G + head_in) * kD : -1;
+      // Writes 64 columns of the warp's rows, each lane giving its own, by way of shared
+      // memory: a row's 16 bytes per lane would take 32 lines for every store.
+      auto put = [&](int half, const float* o, float r) {
+        unsigned char* buf = s.out[warp];
+        __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 128; ++e) o[e] = 0.0f;
-            for (int c = d.c0; c <= d.c1 && !bad; ++c) {
-              const float* p = part_of(a, c, c == d.c0, x);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p) + row);
-              const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
-              sum += ml.y * f;
+        for (int e = 0; e < 8; ++e) {
+          uint4 w;
+          w.x = pack2<F16>(o[8 * e] * r, o[8 * e + 1] * r);
+          w.y = pack2<F16>(o[8 * e + 2] * r, o[8 * e + 3] * r);
+          w.z = pack2<F16>(o[8 * e + 4] * r, o[8 * e + 5] * r);
+          w.w = pack2<F16>(o[8 * e + 6] * r, o[8 * e + 7] * r);
+          *reinterpret_cast<uint4*>(buf + lane * 128 + ((e ^ (lane & 7)) << 4)) = w;
+        }
+        __syncwarp();
 #pragma unroll
-              for (int e = 0; e < 128; e += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows) + (e / 4) * kRows + row);
-                o[e] += v.x * f, o[e + 1] += v.y * f, o[e + 2] += v.z * f, o[e + 3] += v.w * f;
-              }
-            }
-            const float rs = bad ? 0.0f : 1.0f / sum;
+        for (int i = 0; i < 8; ++i) {
+          const int from = 4 * i + (lane >> 3), e = lane & 7;
+          const long long dst = __shfl_sync(0xffffffffu, at, from);
+          const uint4 w = *reinterpret_cast<const uint4*>(buf + from * 128 + ((e ^ (from & 7)) << 4));
+          if (dst >= 0) *reinterpret_cast<uint4*>(a.out + dst + 64 * half + 8 * e) = w;
+        }
+      };
+      auto sums = [&](int half, float* o) {  // 64 columns of O
+        if (some) {
+          tmem_ld32(to + 64 * half, o);
+          tmem_ld32(to + 64 * half + 32, o + 32);
+          tmem_wait_ld();
+          if (both) {
 #pragma unroll
-            for (int e = 0; e < 128; e += 8) {
-              uint4 w;
-              w.x = pack2<F16>(o[e] * rs, o[e + 1] * rs);
-              w.y = pack2<F16>(o[e + 2] * rs, o[e + 3] * rs);
-              w.z = pack2<F16>(o[e + 4] * rs, o[e + 5] * rs);
-              w.w = pack2<F16>(o[e + 6] * rs, o[e + 7] * rs);
-              reinterpret_cast<uint4*>(dst + e)[0] = w;
+            for (int i = 0; i < 64; i += 32) {
+              float v[32];
+              tmem_ld32(to + kRows + 64 * half + i, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[i + e] = o[i + e] * fa + v[e] * fb;
             }
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) o[e] = 0.0f;
         }
+      };
+      if (whole) {
+        const float r = some ? 1.0f / l : 0.0f;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          float o[64];
+          sums(half, o);
+          put(half, o, r);
+        }
+      } else {
+        // ---- the unit is shared: the last tile to arrive joins the others' sums with its own
+        if (d.bad) l = -1.0f;  // a sum below 0 marks a bad page
+        if (!tile_sync()) return;
+        bool join = s.arrived[x][n & 1] == shares - 1;
+        if (!join) {
+          float* mine = part_of(a, blockIdx.x, d.first, x);
+          if (live) reinterpret_cast<float2*>(mine)[row] = make_float2(m, l);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            float o[64];
+            __syncwarp();
+            sums(half, o);
+            if (live)
+#pragma unroll
+              for (int e = 0; e < 64; e += 4)
+                reinterpret_cast<float4*>(mine + 2 * kRows)[(16 * half + e / 4) * kRows + row] =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+          __threadfence();
+          if (!tile_sync()) return;
+          if (row == 0) s.arrived[x][n & 1] = atomicAdd(ticket, 1);
+          if (!tile_sync()) return;
+          join = s.arrived[x][n & 1] == shares - 1;
+        }
+        if (join) {
+          __threadfence();
+          if (row == 0) *ticket = 0;
+          float top = m;
+          bool bad = d.bad;
+          for (int c = d.c0; c <= d.c1; ++c) {
+            if (!live || c == static_cast<int>(blockIdx.x)) continue;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(a, c, c == d.c0, x)) + row);
+            top = fmaxf(top, ml.x);
+            bad |= ml.y < 0.0f;
+          }
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            float sum = 0.0f, o[64];
+#pragma unroll
+            for (int e = 0; e < 64; ++e) o[e] = 0.0f;
+            for (int c = d.c0; c <= d.c1; ++c) {  // in order, whoever joins
+              if (c == static_cast<int>(blockIdx.x)) {
+                const float f = m == -INFINITY ? 0.0f : ex2((m - top) * a.c);
+                sum += l * f;
+                float v[64];
+                __syncwarp();
+                sums(half, v);
+                if (f > 0.0f)
+#pragma unroll
+                  for (int e = 0; e < 64; ++e) o[e] += v[e] * f;
+              } else if (live) {
+                const float* p = part_of(a, c, c == d.c0, x);
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p) + row);
+                float4 v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  v[e] = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows) + (16 * half + e) * kRows + row);
+                const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
+                sum += ml.y * f;
+                if (f > 0.0f)
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    o[4 * e] += v[e].x * f, o[4 * e + 1] += v[e].y * f, o[4 * e + 2] += v[e].z * f, o[4 * e + 3] += v[e].w * f;
+              }
+            }
+            if (bad) {
+#pragma unroll
+              for (int e = 0; e < 64; ++e) o[e] = 0.0f;
+            }
+            put(half, o, bad ? 0.0f : 1.0f / sum);
+          }
+        }
+      }
+      if (d.twin) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.twin_empty);
       }
     }
     it += 2 * d.steps;
@@ -641,7 +878,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CrossArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&s.tmem)),
+                 "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  if (tid == 32 * kLoadWarp) {
+    prefetch_map(&kv_map);
+    prefetch_map(&q_map);
+  }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.kv_full[i], 1);
@@ -650,85 +897,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&s.q_full, 1);
     mbar_init(&s.q_empty, 1);
     mbar_init(&s.drain, 1);
+    mbar_init(&s.twin_full, 4);
+    mbar_init(&s.twin_empty, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.part_full[i], 1);
       mbar_init(&s.part_empty[i], 9);  // the eight row warps and the MMA thread
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 4);
+      mbar_init(&s.p_full[i][0], 4);
+      mbar_init(&s.p_full[i][1], 4);
       mbar_init(&s.o_full[i], 1);
       mbar_init(&s.join[i], 4);
     }
     s.dead = 0;
     fence_mbar_init();
   }
-  griddep_wait();
-  griddep_launch_dependents();
-  // steps of all sequences (thread i: the i-th share of them), the longest sequence, and
-  // the sequence of this CTA's first step
-  const int per = (a.n_seq + kThreads - 1) / kThreads;
-  const int s0 = min(a.n_seq, tid * per), s1 = min(a.n_seq, s0 + per);
-  long long mine = 0;
-  int longest = 0;
-  bool bad = false;
-  for (int i = s0; i < s1; ++i) {
-    const Seq q = seq_of(a, i);
-    bad |= q.bad;
-    mine += static_cast<long long>(q.steps) * q.blocks;
-    if (q.blocks) longest = max(longest, q.steps);
-  }
-  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_BAD_POS));
-  mine *= a.H;
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 31) {
-    s.warp_sum[warp] = incl;
-    s.warp_max[warp] = longest;
-  }
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s.warp_sum[w];
-    total += s.warp_sum[w];
-    longest = max(longest, s.warp_max[w]);
-  }
-  // A run of r steps saves (longest / r) joins of about half a step each at the end of a
-  // unit: no run shorter than sqrt(longest / 2).
-  const int shortest = max(1, static_cast<int>(sqrtf(0.5f * static_cast<float>(longest))));
-  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + shortest - 1) / shortest));
-  if (static_cast<int>(blockIdx.x) >= n_cta) return;  // the whole CTA
-  const long long f0 = run_start(blockIdx.x, n_cta, total), f1 = run_start(blockIdx.x + 1, n_cta, total);
-  if (before <= f0 && f0 < before + mine) {
-    long long b = before;
-    int i = s0;
-    for (; i < s1 - 1; ++i) {
-      const Seq q = seq_of(a, i);
-      const long long n = static_cast<long long>(q.steps) * q.blocks * a.H;
-      if (f0 < b + n) break;
-      b += n;
-    }
-    s.first_seq = i;
-    s.first_step = b;
-    s.total = total;
-  }
-  __syncwarp();
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&s.tmem)),
-                 "n"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem;
+  griddep_wait();
+  griddep_launch_dependents();
   if (warp >= kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp) load_role(a, s, &kv_map, &q_map, f0, f1, n_cta);
+    if (warp == kLoadWarp) load_role(a, s, &kv_map, &q_map);
     if (warp == kMmaWarp) mma_role<F16>(a, s, tmem);
     __syncwarp();
   } else {

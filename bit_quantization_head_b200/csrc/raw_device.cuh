@@ -8,19 +8,39 @@
 namespace kvtc {
 namespace raw {
 
+// a / b for a >= 0, b > 0, in 32 bits where they do (a 64-bit division takes a few hundred
+// cycles at the head of every launch).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // All tiles of all units in a row, cut into one run per CTA: the tile at which CTA i of n
 // starts, and the CTA that holds tile t.
-__device__ __forceinline__ long long run_start(long long i, long long n, long long total) { return i * total / n; }
+__device__ __forceinline__ long long run_start(long long i, long long n, long long total) { return divide(i * total, n); }
 __device__ __forceinline__ int run_owner(long long t, long long n, long long total) {
-  return static_cast<int>(((t + 1) * n + total - 1) / total) - 1;
+  return static_cast<int>(divide((t + 1) * n + total - 1, total)) - 1;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // Bounded wait (2^16 sleeps of up to 20 us), given up at once when the CTA is dead.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t phase, volatile int* dead) {
-  if (mbar_try_wait(bar, phase)) return true;
   for (uint32_t i = 0; i < (1u << 16); ++i) {
     if (mbar_try_wait_sleep(bar, phase, 20000u)) return true;
     if (*dead) return false;
+  }
+  return false;
+}
+
+// The same by a whole warp, which stays together.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t phase, volatile int* dead) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase))) return true;
+  for (uint32_t i = 0; i < (1u << 16); ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, phase, 20000u))) return true;
+    if (__any_sync(0xffffffffu, *dead)) return false;
   }
   return false;
 }
