@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <utility>
 
@@ -58,19 +59,32 @@ inline kvtc_status check_attention(const kvtc_raw_cache* c, int layer, int n_q_h
 
 // SM count of the current device (a constant of the device, read once for each).
 inline kvtc_status sm_count(int* out) {
-  static int known[64] = {};
+  static std::atomic<int> known[64];
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (dev >= 0 && dev < 64 && known[dev] > 0) {
-    *out = known[dev];
-    return KVTC_OK;
-  }
+  if (dev >= 0 && dev < 64 && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return KVTC_OK;
   int n = 0;
   e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess || n < 1) return cuda_fail(e, "device query");
-  if (dev >= 0 && dev < 64) known[dev] = n;
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   *out = n;
+  return KVTC_OK;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device (set once for
+// each device).
+template <auto Kernel>
+inline kvtc_status allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return KVTC_OK;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  done.fetch_or(bit, std::memory_order_relaxed);
   return KVTC_OK;
 }
 

@@ -48,6 +48,9 @@ constexpr uint32_t kTmemCols = 512;              // S_a, S_b, O_a, O_b
 // Registers of a thread: 384 threads start with 168 each (64512); the row warps take what
 // the others leave (2 * 216 + 72 = 3 * 168).
 constexpr int kRowRegs = 216, kOtherRegs = 72;
+// What a unit costs beside its steps (filling the pipeline, output or parts), in steps: the
+// runs are cut by steps + kUnitCost slots a unit, the first kUnitCost of them without a step.
+constexpr int kUnitCost = 3;
 // Steps of a unit of one tile from which the second tile takes every other one.
 constexpr int kTwinSteps = 4;
 // Pairs of eight whose weights are formed on the FMA pipe.
@@ -275,7 +278,7 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
 __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map, const CUtensorMap* q_map) {
   const int lane = threadIdx.x & 31;
   volatile int* dead = &s.dead;
-  // steps of all sequences and the longest one
+  // slots of all sequences and the longest one's steps
   long long total = 0;
   int longest = 0;
   bool bad_seq = false;
@@ -283,7 +286,7 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
   for (int i = lane; i < a.n_seq; i += 32) {
     sq = seq_of(a, i);
     bad_seq |= sq.bad;
-    total += static_cast<long long>(sq.steps) * sq.blocks;
+    total += static_cast<long long>(sq.steps + kUnitCost) * sq.blocks;
     if (sq.blocks) longest = max(longest, sq.steps);
   }
 #pragma unroll
@@ -299,19 +302,14 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
   if (static_cast<int>(blockIdx.x) < n_cta) {
     f = run_start(blockIdx.x, n_cta, total);
     f1 = run_start(blockIdx.x + 1, n_cta, total);
-  } else if (lane == 0) {  // nothing for this CTA
-    Part d = {};
-    d.first = d.last = d.end = 1;
-    s.part[0] = d;
-    mbar_arrive(&s.part_full[0]);
   }
-  // the sequence of the run's first step
+  // the sequence of the run's first slot
   int seq = 0, n_part = 0, n_q = 0, it = 0;
-  long long base = 0;  // first step of the sequence's units
+  long long base = 0;  // first slot of the sequence's units
   for (int i0 = 0; f < f1; i0 += 32) {
     const int i = i0 + lane;
     if (a.n_seq > 32) sq = seq_of(a, min(i, a.n_seq - 1));
-    const long long mine = i < a.n_seq ? static_cast<long long>(sq.steps) * sq.blocks * a.H : 0;
+    const long long mine = i < a.n_seq ? static_cast<long long>(sq.steps + kUnitCost) * sq.blocks * a.H : 0;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -340,14 +338,16 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
     return true;
   };
   while (f < f1 && ok) {
-    while (f >= base + static_cast<long long>(sq.steps) * a.H * sq.blocks) {
-      base += static_cast<long long>(sq.steps) * a.H * sq.blocks;
+    while (f >= base + static_cast<long long>(sq.steps + kUnitCost) * a.H * sq.blocks) {
+      base += static_cast<long long>(sq.steps + kUnitCost) * a.H * sq.blocks;
       sq = seq_of(a, ++seq);
     }
-    const int u = static_cast<int>(divide(f - base, sq.steps)), h = u / sq.blocks, blk = u - h * sq.blocks;
-    const long long begin = base + static_cast<long long>(u) * sq.steps;
-    const int i0 = static_cast<int>(f - begin);
-    const int i1 = static_cast<int>(min(static_cast<long long>(sq.steps), i0 + (f1 - f)));
+    const int u = static_cast<int>(divide(f - base, sq.steps + kUnitCost)), h = u / sq.blocks, blk = u - h * sq.blocks;
+    const long long begin = base + static_cast<long long>(u) * (sq.steps + kUnitCost) + kUnitCost;  // its first step
+    const int i0 = static_cast<int>(max(0ll, f - begin));
+    const int i1 = static_cast<int>(min(static_cast<long long>(sq.steps), f1 - begin));
+    f = begin + sq.steps;
+    if (i1 <= i0) break;  // the run ends before the unit's first step
     const int32_t* pages = a.table + static_cast<size_t>(seq) * a.max_pages;
     bool good = true;
     int ids = 0;  // the next 32 page ids, one per lane
@@ -377,8 +377,8 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
     d.bad = !good;
     d.c0 = run_owner(begin, n_cta, total);
     d.c1 = run_owner(begin + sq.steps - 1, n_cta, total);
-    f += i1 - i0;
-    d.end = f >= f1;
+    d.end = f1 - f <= kUnitCost;  // no step of the next unit
+    if (d.end) f = f1;
     if (lane == 0) {
       if (n_part >= 2) ok = wait_phase(&s.part_empty[n_part & 1], ((n_part >> 1) - 1) & 1, dead);
       if (ok) {
@@ -409,6 +409,12 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
       }
     }
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  }
+  if (n_part == 0 && lane == 0) {  // nothing for this CTA
+    Part d = {};
+    d.first = d.last = d.end = 1;
+    s.part[0] = d;
+    mbar_arrive(&s.part_full[0]);
   }
   if (lane == 0) {
     if (!ok) {
@@ -945,10 +951,9 @@ template <bool F16>
 kvtc_status launch_cross(const CUtensorMap& kv_map, const CUtensorMap& q_map, const CrossArgs& a, int grid,
                          void* stream) {
   const size_t smem = sizeof(Smem) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(raw_cross_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (raw cross)");
-  e = launch(raw_cross_kernel<F16>, dim3(static_cast<unsigned>(grid)), kThreads, smem, stream, kv_map, q_map, a);
+  const kvtc_status st = allow_smem<raw_cross_kernel<F16>>(smem);
+  if (st != KVTC_OK) return st;
+  const cudaError_t e = launch(raw_cross_kernel<F16>, dim3(static_cast<unsigned>(grid)), kThreads, smem, stream, kv_map, q_map, a);
   if (e != cudaSuccess) return cuda_fail(e, "raw cross launch");
   return KVTC_OK;
 }

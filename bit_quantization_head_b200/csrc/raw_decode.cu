@@ -543,10 +543,9 @@ CUtensorMapDataType map_type(kvtc_dtype t) {
 template <int NT, bool F16>
 kvtc_status launch_decode(const CUtensorMap& map, const DecodeArgs& a, int grid, void* stream) {
   const size_t smem = sizeof(Smem<NT>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(raw_decode_kernel<NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute (raw decode)");
-  e = launch(raw_decode_kernel<NT, F16>, dim3(static_cast<unsigned>(grid)), kThreads, smem, stream, map, a);
+  const kvtc_status st = allow_smem<raw_decode_kernel<NT, F16>>(smem);
+  if (st != KVTC_OK) return st;
+  const cudaError_t e = launch(raw_decode_kernel<NT, F16>, dim3(static_cast<unsigned>(grid)), kThreads, smem, stream, map, a);
   if (e != cudaSuccess) return cuda_fail(e, "raw decode launch");
   return KVTC_OK;
 }

@@ -158,6 +158,15 @@ def _stream(stream):
     return _P(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
 
 
+def _stream_on(device, stream):
+    """The same for a call whose device is known (a few us less than the public lookup)."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return _stream(None) if raw is None else raw(device)
+
+
 def _dtype_code(t):
     import torch
     if t.dtype == torch.bfloat16:
@@ -348,58 +357,85 @@ def kvtc_decode_attention_rope(plan, cache, layer, q, seq_lens, max_seq_len, out
 
 
 # ---------------------------------------------------------------- serving step
-_I32, _I64 = "torch.int32", "torch.int64"
-_RAW_DTYPES = {"torch.float32": KVTC_F32, "torch.bfloat16": KVTC_BF16, "torch.float16": KVTC_F16}
+# Checks of these calls read each tensor's properties once and compare objects, not texts:
+# a call of the smallest sizes is bound by the host (about 36 us before, 8 us after for the
+# twelve tensors of kvtc_step_tables).
+_raw_dtypes = {}
 
 
-def _buf(t, dtype, name, shape=None):
-    """Device pointer of a contiguous tensor on the current device, of one dtype (and shape)."""
+def _raw_dtype(dtype):
+    """Library code of a torch dtype that the calls around the cache take."""
+    if not _raw_dtypes:
+        import torch
+        _raw_dtypes.update({torch.float32: KVTC_F32, torch.bfloat16: KVTC_BF16, torch.float16: KVTC_F16})
+    code = _raw_dtypes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _device(t, name):
+    """Index of the device of a tensor, which must be the current one."""
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    d = t.get_device()
+    if d < 0 or d != torch.cuda.current_device():
         raise ValueError(f"{name} must be on the current CUDA device")
-    if str(t.dtype) != dtype:
+    return d
+
+
+def _buf(t, dtype, name, device, shape=None):
+    """Device pointer of a contiguous tensor on one device, of one dtype (and shape)."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _rows(t, dtype, name, n_tok=None):
+def _rows(t, dtype, name, device, n_tok):
     """(pointer, token stride, heads) of rows [n_tok][heads][128] whose heads and elements
     are dense (a slice of a fused projection passes as it is)."""
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != device:
         raise ValueError(f"{name} must be on the current CUDA device")
-    if str(t.dtype) != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or (n_tok is not None and t.shape[0] != n_tok):
-        raise ValueError(f"{name} must have shape [n_tok][heads][{HEAD_DIM}], got {tuple(t.shape)}")
-    n, heads, _ = t.shape
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != HEAD_DIM or shape[0] != n_tok:
+        raise ValueError(f"{name} must have shape [n_tok][heads][{HEAD_DIM}], got {tuple(shape)}")
+    heads = shape[1]
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != HEAD_DIM):
         raise ValueError(f"{name}: heads and elements must be dense")
-    return t.data_ptr(), (t.stride(0) if n > 1 else max(heads * HEAD_DIM, 1)), heads
+    return t.data_ptr(), (stride[0] if n_tok > 1 else max(heads * HEAD_DIM, 1)), heads
 
 
 def kvtc_step_tables(cached_lens, new_lens, page_ring, ring_state, block_table, seq_lens, cu_seqlens, slot_map,
                      positions, ring_state_out, workspace, status=None, stream=None):
     """Tables of one serving step from the request lengths (all device tensors; int32, the
     slot map int64).  ring_state_out may be ring_state and seq_lens may be cached_lens."""
+    import torch
+    i32, dev = torch.int32, _device(cached_lens, "cached_lens")
     n_seq, rows = cached_lens.numel(), slot_map.numel()
     if block_table.dim() != 2:
         raise ValueError("block_table must have shape [n_seq][max_pages]")
     max_pages = block_table.shape[1]
-    if workspace.numel() * workspace.element_size() < 16:
+    if workspace.nbytes < 16:
         raise ValueError("workspace must hold 16 bytes")
-    _check(lib().kvtc_step_tables(
-        _buf(cached_lens, _I32, "cached_lens"), _buf(new_lens, _I32, "new_lens", (n_seq,)), n_seq,
-        _buf(page_ring, _I32, "page_ring"), page_ring.numel(), _buf(ring_state, _I32, "ring_state", (2,)),
-        _buf(block_table, _I32, "block_table", (n_seq, max_pages)), max_pages,
-        _buf(seq_lens, _I32, "seq_lens", (n_seq,)), _buf(cu_seqlens, _I32, "cu_seqlens", (n_seq + 1,)),
-        _buf(slot_map, _I64, "slot_map"), _buf(positions, _I32, "positions", (rows,)), rows,
-        _buf(ring_state_out, _I32, "ring_state_out", (2,)), _buf(workspace, str(workspace.dtype), "workspace"),
-        None if status is None else _buf(status, _I32, "status"), _stream(stream)))
+    per_seq = (n_seq,)
+    st = lib().kvtc_step_tables(
+        _buf(cached_lens, i32, "cached_lens", dev), _buf(new_lens, i32, "new_lens", dev, per_seq), n_seq,
+        _buf(page_ring, i32, "page_ring", dev), page_ring.numel(), _buf(ring_state, i32, "ring_state", dev, (2,)),
+        _buf(block_table, i32, "block_table", dev, (n_seq, max_pages)), max_pages,
+        _buf(seq_lens, i32, "seq_lens", dev, per_seq), _buf(cu_seqlens, i32, "cu_seqlens", dev, (n_seq + 1,)),
+        _buf(slot_map, torch.int64, "slot_map", dev), _buf(positions, i32, "positions", dev, (rows,)), rows,
+        _buf(ring_state_out, i32, "ring_state_out", dev, (2,)), _buf(workspace, None, "workspace", dev),
+        None if status is None else _buf(status, i32, "status", dev), _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
 def rope_desc(sections, interleaved=False, base=0.0):
@@ -411,27 +447,32 @@ def rope_desc(sections, interleaved=False, base=0.0):
     return RopeDesc(len(sections), (C.c_int * 4)(*sections), 1 if interleaved else 0, float(base))
 
 
+_NO_ROWS = (None, 0, 0)
+
+
 def kvtc_rope(rope, q, k, positions, q_out, k_out, inverse=False, stream=None):
     """Rotates q and/or k rows [n_tok][heads][128] to positions int32 [n_axes][n_tok]
     (or [n_tok] for one axis); inverse: the transpose.  q or k may be None."""
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    dtype, n_tok = str(ref.dtype), ref.shape[0]
-    if dtype not in _RAW_DTYPES:
-        raise TypeError(f"unsupported dtype {ref.dtype}")
-    qp = _rows(q, dtype, "q", n_tok) if q is not None else (None, 0, 0)
-    kp = _rows(k, dtype, "k", n_tok) if k is not None else (None, 0, 0)
-    _check(lib().kvtc_rope(
-        C.byref(rope), *qp, *kp, _RAW_DTYPES[dtype], _positions_ptr(rope, positions, n_tok), n_tok,
-        1 if inverse else 0, None if q is None else _buf(q_out, dtype, "q_out", tuple(q.shape)),
-        None if k is None else _buf(k_out, dtype, "k_out", tuple(k.shape)), _stream(stream)))
+    dtype, n_tok = ref.dtype, ref.shape[0]
+    code, dev = _raw_dtype(dtype), _device(ref, "q" if q is not None else "k")
+    qp = _rows(q, dtype, "q", dev, n_tok) if q is not None else _NO_ROWS
+    kp = _rows(k, dtype, "k", dev, n_tok) if k is not None else _NO_ROWS
+    st = lib().kvtc_rope(
+        C.byref(rope), *qp, *kp, code, _positions_ptr(rope, positions, n_tok, dev), n_tok, 1 if inverse else 0,
+        None if q is None else _buf(q_out, dtype, "q_out", dev, q.shape),
+        None if k is None else _buf(k_out, dtype, "k_out", dev, k.shape), _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
-def _positions_ptr(rope, positions, n_tok):
+def _positions_ptr(rope, positions, n_tok, device):
+    import torch
     if positions.numel() != rope.n_axes * n_tok or positions.shape[-1] != n_tok:
         raise ValueError(f"positions must have shape [{rope.n_axes}][{n_tok}]")
-    return _buf(positions, _I32, "positions")
+    return _buf(positions, torch.int32, "positions", device)
 
 
 # ---------------------------------------------------------------- uncompressed pages
@@ -458,33 +499,32 @@ class RawCache:
         self.pool = pool
         self.block_table = block_table.to(device=pool.device, dtype=torch.int32).contiguous()
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
-        self.dtype = str(dtype)
+        self.dtype = dtype
         self.n_kv_heads = shape[2]
-        self.desc = RawCacheDesc(pool.data_ptr(), shape[0], shape[1], shape[2], _RAW_DTYPES[self.dtype],
-                                 self.block_table.data_ptr(), self.block_table.shape[0], self.block_table.shape[1],
+        self.n_seq = self.block_table.shape[0]
+        self.desc = RawCacheDesc(pool.data_ptr(), shape[0], shape[1], shape[2], _raw_dtype(dtype),
+                                 self.block_table.data_ptr(), self.n_seq, self.block_table.shape[1],
                                  self.status.data_ptr())
-
-    def _on_current_device(self):
-        import torch
-        if self.pool.device.index != torch.cuda.current_device():
-            raise ValueError("the cache must be on the current CUDA device")
-        return C.byref(self.desc)
 
 
 def kvtc_raw_append(cache, layer, k, v, slot_map, rope=None, positions=None, q=None, q_out=None, stream=None):
     """Writes k, v rows [n_tok][n_kv_heads][128] into their slots (int64 [n_tok]) of one
     layer's pages; with rope, k is rotated on the way, and q into q_out."""
-    n_tok, dtype = k.shape[0], cache.dtype
-    kp, vp = _rows(k, dtype, "k", n_tok), _rows(v, dtype, "v", n_tok)
+    import torch
+    n_tok, dtype, dev = k.shape[0], cache.dtype, _device(cache.pool, "the cache")
+    kp, vp = _rows(k, dtype, "k", dev, n_tok), _rows(v, dtype, "v", dev, n_tok)
     if kp[2] != cache.n_kv_heads or vp[2] != cache.n_kv_heads:
         raise ValueError(f"k and v must have {cache.n_kv_heads} heads")
     if rope is not None and positions is None:
         raise ValueError("rope needs positions")
-    qp = _rows(q, dtype, "q", n_tok) if q is not None else (None, 0, 0)
-    _check(lib().kvtc_raw_append(
-        cache._on_current_device(), layer, kp[0], kp[1], vp[0], vp[1], _buf(slot_map, _I64, "slot_map", (n_tok,)), n_tok,
-        None if rope is None else C.byref(rope), None if rope is None else _positions_ptr(rope, positions, n_tok),
-        *qp, None if q is None else _buf(q_out, dtype, "q_out", tuple(q.shape)), _stream(stream)))
+    qp = _rows(q, dtype, "q", dev, n_tok) if q is not None else _NO_ROWS
+    st = lib().kvtc_raw_append(
+        C.byref(cache.desc), layer, kp[0], kp[1], vp[0], vp[1], _buf(slot_map, torch.int64, "slot_map", dev, (n_tok,)),
+        n_tok, None if rope is None else C.byref(rope),
+        None if rope is None else _positions_ptr(rope, positions, n_tok, dev), *qp,
+        None if q is None else _buf(q_out, dtype, "q_out", dev, q.shape), _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
 def kvtc_raw_decode_workspace_bytes(n_seq, n_q_heads, n_kv_heads, max_seq_len):
@@ -495,30 +535,37 @@ def kvtc_raw_cross_workspace_bytes(n_seq, n_tok, n_q_heads, n_kv_heads, max_seq_
     return int(lib().kvtc_raw_cross_workspace_bytes(n_seq, n_tok, n_q_heads, n_kv_heads, max_seq_len))
 
 
-def _head_rows(cache, t, name, rows):
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != HEAD_DIM:
-        raise ValueError(f"{name} must have shape [{rows}][n_q_heads][{HEAD_DIM}], got {tuple(t.shape)}")
-    return _buf(t, cache.dtype, name)
+def _head_rows(cache, t, name, rows, device):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must have shape [{rows}][n_q_heads][{HEAD_DIM}], got {tuple(shape)}")
+    return _buf(t, cache.dtype, name, device)
 
 
 def kvtc_raw_decode_attention(cache, layer, q, seq_lens, max_seq_len, out, workspace, scale=0.0, stream=None):
     """One new token per sequence over one layer's uncompressed pages; q, out
     [n_seq][n_q_heads][128] of the cache's dtype."""
-    n_seq = cache.desc.n_seq
-    qp = _head_rows(cache, q, "q", n_seq)
-    _check(lib().kvtc_raw_decode_attention(
-        cache._on_current_device(), layer, qp, q.shape[1], _buf(seq_lens, _I32, "seq_lens", (n_seq,)), max_seq_len,
-        scale, _buf(out, cache.dtype, "out", tuple(q.shape)), _buf(workspace, str(workspace.dtype), "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    import torch
+    n_seq, dev = cache.n_seq, _device(cache.pool, "the cache")
+    st = lib().kvtc_raw_decode_attention(
+        C.byref(cache.desc), layer, _head_rows(cache, q, "q", n_seq, dev), q.shape[1],
+        _buf(seq_lens, torch.int32, "seq_lens", dev, (n_seq,)), max_seq_len, scale,
+        _buf(out, cache.dtype, "out", dev, q.shape), _buf(workspace, None, "workspace", dev), workspace.nbytes,
+        _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
 def kvtc_raw_cross_attention(cache, layer, q, cu_q, seq_lens, max_seq_len, out, workspace, scale=0.0, stream=None):
     """Rows cu_q[s]..cu_q[s+1]-1 of q [n_tok][n_q_heads][128] attend to the first seq_lens[s]
     tokens of sequence s's uncompressed pages (no causal mask)."""
-    n_seq = cache.desc.n_seq
-    qp = _head_rows(cache, q, "q", q.shape[0])
-    _check(lib().kvtc_raw_cross_attention(
-        cache._on_current_device(), layer, qp, q.shape[1], _buf(cu_q, _I32, "cu_q", (n_seq + 1,)), q.shape[0],
-        _buf(seq_lens, _I32, "seq_lens", (n_seq,)), max_seq_len, scale, _buf(out, cache.dtype, "out", tuple(q.shape)),
-        _buf(workspace, str(workspace.dtype), "workspace"), workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+    import torch
+    n_seq, n_tok, dev = cache.n_seq, q.shape[0], _device(cache.pool, "the cache")
+    st = lib().kvtc_raw_cross_attention(
+        C.byref(cache.desc), layer, _head_rows(cache, q, "q", n_tok, dev), q.shape[1],
+        _buf(cu_q, torch.int32, "cu_q", dev, (n_seq + 1,)), n_tok,
+        _buf(seq_lens, torch.int32, "seq_lens", dev, (n_seq,)), max_seq_len, scale,
+        _buf(out, cache.dtype, "out", dev, q.shape), _buf(workspace, None, "workspace", dev), workspace.nbytes,
+        _stream_on(dev, stream))
+    if st:
+        _check(st)
