@@ -7,27 +7,33 @@
 // t - rint(t) (at p = 1e5 an fp32 angle is off by about 1e-2 rad), its cosine and sine and
 // the rotation are fp32, rounded once to the rows' type.
 //
-// Bound: memory, each row read and written once.  One kernel serves both calls: a CTA takes
-// a few tokens with all their heads, so the 64 (cos, sin) pairs of a token are made once in
-// shared memory for its q and k heads; a thread moves 16 bytes at i and 16 at i + 64, so a
-// rotation needs no exchange between threads.  The loads of a batch of rows are issued
-// before the sines are made.
+// Bound: memory, each row read and written once.  One kernel serves both calls: a warp takes
+// a token's rows, 16 bytes at i and 16 at i + 64 of a row per lane, so a rotation needs no
+// exchange and a lane meets the same pairs in every row: it keeps their cosines and sines in
+// registers.  The token's 64 are made once, two (cos, sin) per lane, and dealt through the
+// warp's shared memory, after the loads of the first rows have been issued; warps never wait
+// for one another (a block of a few tokens that shared them behind a barrier reached 3.3 TB/s,
+// at two blocks per SM).  Few tokens: a token's rows are dealt over several warps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "raw_cache.cuh"
+#include "raw_device.cuh"
 
 namespace kvtc {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kHalf = kD / 2;
-constexpr int kMaxTok = 16;  // tokens of one CTA
+constexpr int kBatch = 4;            // rows of a lane in flight
+constexpr int kBusyWarps = 148 * 48;  // two rounds of warps on every SM: one of 1.15 left a tail (4097 fp32 rows of 32 heads 26.6 us, two 23.9, eight 31.7)
 
 struct RopeArgs {
   const void* x[3];        // q, k, v (null: absent)
@@ -41,114 +47,107 @@ struct RopeArgs {
   int page_heads;
   const int32_t* positions;
   int n_tok;
-  int tok_per_cta;
+  int parts, part_rows;    // warps of a token, rows of each
   int rotate;
   int32_t* status;
   double turns[kHalf];     // +-f_i / 2 pi
   uint8_t axis[kHalf];
 };
 
+// Two elements of a 32-bit word (one for fp32, whose second is not used).
 template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_f<__half>(__half x) { return __half2float(x); }
+__device__ __forceinline__ float2 unpack(uint32_t w) {
+  if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w), 0.0f);
+  if constexpr (std::is_same_v<T, __half>) return half2_to_float2(w);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
 template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+  if constexpr (sizeof(T) == 4) return __float_as_uint(x);
+  return raw::pack2<std::is_same_v<T, __half>>(x, y);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // elements of a 16-byte chunk
-  constexpr int kLanes = kHalf / kVec;                     // threads of a row
-  constexpr int kRows = kThreads / kLanes;                 // rows moved at a time
-  constexpr int kBatch = 4;                                // rows of a thread in flight
-  __shared__ float2 cs[kMaxTok][kHalf];
-  __shared__ long long slot_of[kMaxTok];
+  constexpr int kPer = kVec / 4;                           // elements of a 32-bit word
+  constexpr int kLanes = kHalf / kVec;                     // lanes of a row
+  constexpr int kRows = 32 / kLanes;                       // rows moved at a time
+  __shared__ float2 cs[kWarps][kHalf];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, ch = tid % kLanes;
-  const int tok0 = static_cast<int>(blockIdx.x) * a.tok_per_cta;
-  const int n_tok = min(a.tok_per_cta, a.n_tok - tok0);
-  const int per_tok = a.heads[0] + a.heads[1] + a.heads[2];
-  const int n_rows = n_tok * per_tok;
-  for (int first = 0; first < n_rows; first += kRows * kBatch) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = lane % kLanes;
+  const long long w = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const int tok = static_cast<int>(a.parts == 1 ? w : w / a.parts);
+  if (w >= static_cast<long long>(a.n_tok) * a.parts) return;  // the whole warp
+  const int part = static_cast<int>(w - static_cast<long long>(tok) * a.parts);
+  const int nq = a.heads[0], nqk = nq + a.heads[1], n_all = nqk + a.heads[2];
+  const int r0 = part * a.part_rows, r1 = min(n_all, r0 + a.part_rows);
+  long long slot = 0;
+  if (a.slots) {
+    slot = a.slots[tok];
+    if (slot >= a.n_slots) {
+      if (lane == 0 && part == 0 && a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_BAD_PAGE));
+      slot = -1;
+    }
+  }
+  const int end = slot < 0 ? min(r1, nq) : r1;  // rows of k and v without a slot are skipped
+  float cn[kVec], sn[kVec];
+  for (int first = r0; first < end || first == r0; first += kRows * kBatch) {
     uint4 lo[kBatch], hi[kBatch];
-    int tk[kBatch], hd[kBatch], kind[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int row = first + b * kRows + tid / kLanes;
-      kind[b] = -1;
-      if (row < n_rows) {
-        tk[b] = row / per_tok;
-        int h = row - tk[b] * per_tok, kd = 0;
-        if (h >= a.heads[0]) h -= a.heads[0], kd = 1;
-        if (kd == 1 && h >= a.heads[1]) h -= a.heads[1], kd = 2;
-        hd[b] = h;
-        kind[b] = kd;
-        const T* src = static_cast<const T*>(a.x[kd]) + static_cast<long long>(tok0 + tk[b]) * a.stride[kd] +
-                       static_cast<long long>(h) * kD + ch * kVec;
+      const int r = first + b * kRows + lane / kLanes;
+      if (r < end) {
+        const int kd = r < nq ? 0 : r < nqk ? 1 : 2, h = r - (kd == 0 ? 0 : kd == 1 ? nq : nqk);
+        const char* src = static_cast<const char*>(kd == 0 ? a.x[0] : kd == 1 ? a.x[1] : a.x[2]) +
+                          (static_cast<long long>(tok) * (kd == 0 ? a.stride[0] : kd == 1 ? a.stride[1] : a.stride[2]) +
+                           h * kD) * static_cast<long long>(sizeof(T)) + ch * 16;
         lo[b] = *reinterpret_cast<const uint4*>(src);
-        hi[b] = *reinterpret_cast<const uint4*>(src + kHalf);
+        hi[b] = *reinterpret_cast<const uint4*>(src + kHalf * sizeof(T));
       }
     }
-    if (first == 0) {
-      if (a.rotate)
-        for (int e = tid; e < n_tok * kHalf; e += kThreads) {
-          const int t = e / kHalf, i = e % kHalf;
-          const double turn = static_cast<double>(a.positions[static_cast<long long>(a.axis[i]) * a.n_tok + tok0 + t]) * a.turns[i];
-          float sn, cn;
-          sincospif(static_cast<float>(2.0 * (turn - rint(turn))), &sn, &cn);
-          cs[t][i] = make_float2(cn, sn);
-        }
-      if (a.slots && tid < n_tok) {
-        const long long sl = a.slots[tok0 + tid];
-        slot_of[tid] = sl < a.n_slots ? sl : -1;
-        if (sl >= a.n_slots && a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_BAD_PAGE));
+    if (first == r0 && a.rotate) {
+#pragma unroll
+      for (int i = lane; i < kHalf; i += 32) {
+        const double turn = static_cast<double>(a.positions[static_cast<long long>(a.axis[i]) * a.n_tok + tok]) * a.turns[i];
+        float s, c;
+        sincospif(static_cast<float>(2.0 * (turn - rint(turn))), &s, &c);
+        cs[warp][i] = make_float2(c, s);
       }
-      __syncthreads();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kVec; i += 2) {
+        const float4 v = *reinterpret_cast<const float4*>(&cs[warp][ch * kVec + i]);
+        cn[i] = v.x, sn[i] = v.y, cn[i + 1] = v.z, sn[i + 1] = v.w;
+      }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (kind[b] < 0) continue;
-      T* dst;
-      if (kind[b] == 0) {
-        dst = static_cast<T*>(a.q_out) + (static_cast<long long>(tok0 + tk[b]) * a.heads[0] + hd[b]) * kD;
-      } else if (a.slots) {
-        const long long sl = slot_of[tk[b]];
-        if (sl < 0) continue;
-        dst = static_cast<T*>(a.pages) + (((sl / kPage) * a.page_heads + hd[b]) * 2 + (kind[b] - 1)) * raw::kKindElems +
-              (sl % kPage) * kD;
-      } else {
-        dst = static_cast<T*>(a.k_out) + (static_cast<long long>(tok0 + tk[b]) * a.heads[1] + hd[b]) * kD;
-      }
-      dst += ch * kVec;
-      if (a.rotate && kind[b] < 2) {
-        T* l = reinterpret_cast<T*>(&lo[b]);
-        T* h = reinterpret_cast<T*>(&hi[b]);
-        const float4* c4 = reinterpret_cast<const float4*>(&cs[tk[b]][ch * kVec]);
+      const int r = first + b * kRows + lane / kLanes;
+      if (r >= end) continue;
+      const int kd = r < nq ? 0 : r < nqk ? 1 : 2, h = r - (kd == 0 ? 0 : kd == 1 ? nq : nqk);
+      char* dst;
+      if (kd == 0)
+        dst = static_cast<char*>(a.q_out) + (static_cast<long long>(tok) * nq + h) * kD * static_cast<long long>(sizeof(T));
+      else if (a.slots)
+        dst = static_cast<char*>(a.pages) + ((((slot / kPage) * a.page_heads + h) * 2 + (kd - 1)) * raw::kKindElems +
+                                             (slot % kPage) * kD) * static_cast<long long>(sizeof(T));
+      else
+        dst = static_cast<char*>(a.k_out) + (static_cast<long long>(tok) * a.heads[1] + h) * kD * static_cast<long long>(sizeof(T));
+      if (a.rotate && kd < 2) {
+        uint32_t* l = reinterpret_cast<uint32_t*>(&lo[b]);
+        uint32_t* u = reinterpret_cast<uint32_t*>(&hi[b]);
 #pragma unroll
-        for (int i = 0; i < kVec; i += 2) {
-          const float4 v = c4[i / 2];
-          const float c[2] = {v.x, v.z}, s[2] = {v.y, v.w};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float x = to_f<T>(l[i + j]), y = to_f<T>(h[i + j]);
-            l[i + j] = from_f<T>(x * c[j] - y * s[j]);
-            h[i + j] = from_f<T>(y * c[j] + x * s[j]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpack<T>(l[i]), y = unpack<T>(u[i]);
+          const int j = kPer * i, k = kPer * i + kPer - 1;
+          l[i] = pack<T>(x.x * cn[j] - y.x * sn[j], x.y * cn[k] - y.y * sn[k]);
+          u[i] = pack<T>(y.x * cn[j] + x.x * sn[j], y.y * cn[k] + x.y * sn[k]);
         }
       }
-      *reinterpret_cast<uint4*>(dst) = lo[b];
-      *reinterpret_cast<uint4*>(dst + kHalf) = hi[b];
+      *reinterpret_cast<uint4*>(dst + ch * 16) = lo[b];
+      *reinterpret_cast<uint4*>(dst + kHalf * sizeof(T) + ch * 16) = hi[b];
     }
   }
 }
@@ -165,15 +164,19 @@ kvtc_status set_rope(const kvtc_rope_desc* r, bool inverse, RopeArgs& a) {
   if (sum != kHalf) return fail(KVTC_EINVAL, "the sections must sum to 64 pairs");
   const double base = r->base == 0.0 ? 500000.0 : r->base;
   if (!(base > 1.0) || !std::isfinite(base)) return fail(KVTC_EINVAL, "rope base must be 0 or > 1");
-  const double l2 = std::log2(base), two_pi = 6.283185307179586476925;
+  const double two_pi = 6.283185307179586476925;
+  // f_i = base^(-i/64): the powers of two by exp2, the others as products of at most six of
+  // them (a relative error of a few 2^-53, as exp2's own)
+  double f[kHalf];
+  f[0] = 1.0;
+  for (int i = 1; i < kHalf; ++i) f[i] = i & (i - 1) ? f[i & (i - 1)] * f[i & -i] : std::exp2(-std::log2(base) * i / kHalf);
   int ax = 0;
   for (int i = 0; i < kHalf; ++i) {
     while (left[ax] == 0) ax = (ax + 1) % r->n_axes;
     a.axis[i] = static_cast<uint8_t>(ax);
     --left[ax];
     if (r->interleaved) ax = (ax + 1) % r->n_axes;
-    const double f = std::exp2(-l2 * i / kHalf) / two_pi;
-    a.turns[i] = inverse ? -f : f;
+    a.turns[i] = (inverse ? -f[i] : f[i]) / two_pi;
   }
   a.rotate = 1;
   return KVTC_OK;
@@ -214,11 +217,14 @@ kvtc_status check_overlap(const RopeArgs& a, size_t es) {
 }
 
 kvtc_status launch_rope(RopeArgs& a, kvtc_dtype dtype, void* stream) {
-  // tokens of a CTA: about 128 rows (one batch of 4 rows per thread in 16-bit types), so a
-  // few tokens share a launch slot and their sines are spread over the threads
-  const int per_tok = a.heads[0] + a.heads[1] + a.heads[2];
-  a.tok_per_cta = std::min(kMaxTok, std::max(1, 128 / per_tok));
-  const unsigned grid = static_cast<unsigned>((a.n_tok + a.tok_per_cta - 1) / a.tok_per_cta);
+  // as many warps of a token as fill the chip, each with one batch of loads at least
+  const int at_once = dtype == KVTC_F32 ? 2 : 4;  // rows a warp moves at a time
+  const int n_all = a.heads[0] + a.heads[1] + a.heads[2];
+  const int most = (n_all + at_once - 1) / at_once;
+  const int want = std::min(most, (kBusyWarps + a.n_tok - 1) / a.n_tok);
+  a.part_rows = (most + want - 1) / want * at_once;
+  a.parts = (n_all + a.part_rows - 1) / a.part_rows;
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.n_tok) * a.parts + kWarps - 1) / kWarps);
   cudaError_t e;
   if (dtype == KVTC_F32)
     e = raw::launch(rope_kernel<float>, dim3(grid), kThreads, 0, stream, a);

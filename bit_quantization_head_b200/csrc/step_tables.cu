@@ -4,15 +4,17 @@
 // pages a sequence lacks are ceil((c + n) / 128) - ceil(c / 128), and its share of the
 // free ring is the prefix sum of those needs over the sequences that fit.  Whether a
 // sequence fits in the rows depends on the first sum alone, so two block scans decide a
-// chunk of 1024 sequences: (rows, released pages), then (needed pages).
+// chunk of sequences: (rows, released pages), then (needed pages).
 //
 // Bound: latency for a decode step (a launch, two dependent loads, two scans), the 12
 // bytes per row for large steps.  One launch without a wait between CTAs: every CTA scans
 // all sequences for itself (8 bytes each, from L2) and fills its own range of rows; a row
 // finds its sequence by bisection in the chunk's prefix sums in shared memory and takes
 // its page id straight from the ring or the old table entries, so nothing that another
-// CTA writes is read.  The outputs that may replace their inputs (lengths, ring state) are
-// written by the last CTA to finish reading (one counter).
+// CTA writes is read.  Where outputs replace their inputs (lengths, ring state) the last
+// CTA to finish reading writes them (one counter); otherwise the first CTA does, at once.
+// Up to 128 sequences a CTA has 128 threads (a step's barriers and launch cost less), for
+// more 1024 with two sequences each.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -23,9 +25,8 @@
 namespace kvtc {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRowsPerCta = 4096;
+constexpr int kSmallThreads = 128, kLargeThreads = 1024, kLargePer = 2;
+constexpr int kRowsPerThread = 4;
 
 struct TablesArgs {
   const int32_t* cached;
@@ -42,108 +43,137 @@ struct TablesArgs {
   int32_t* positions;
   int n_rows;
   int32_t* state_out;
+  int in_place;     // seq_lens or state_out replace their inputs
   int* ticket;
   int32_t* status;
 };
 
+template <int kThreads, int kPer>
 struct Smem {
-  long long warp_sum[2][kWarps];
-  long long total[2];
-  int first_row[kThreads + 1];  // rows of the chunk's sequences, clipped to n_rows
-  int cached[kThreads];
-  int page0[kThreads];   // ring offset (from the head) of the sequence's first new page
-  int need[kThreads];    // new pages (-1: the sequence keeps its length; -2: finished)
-  int release0[kThreads];  // ring offset (from the tail) of its first released page
+  static constexpr int kWarps = kThreads / 32, kChunk = kThreads * kPer;
+  long long rows_sum[kWarps], released_sum[kWarps];
+  int need_sum[kWarps];
+  int taken;                  // pages taken from the ring's head
   int last;
+  int first_row[kChunk + 1];  // rows of the chunk's sequences, clipped to n_rows
+  int cached[kChunk];
+  int page0[kChunk];          // ring offset (from the head) of the sequence's first new page
+  int need[kChunk];           // new pages (-1: the sequence keeps its length; -2: finished)
+  int release0[kChunk];       // ring offset (from the tail) of its first released page
 };
 
-// Exclusive sums of a and b over the block's threads; totals in s.total.
-__device__ __forceinline__ void scan2(Smem& s, long long& a, long long& b) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = a, y = b;
+// Exclusive sum over the block's warps of one value per thread (incl: the warp's inclusive
+// sums), and the block's total; one barrier, which the caller places between put and get.
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) x += p, y += q;
+    const T p = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += p;
   }
-  if (lane == 31) s.warp_sum[0][warp] = x, s.warp_sum[1][warp] = y;
-  __syncthreads();
-  if (warp < 2) {
-    long long v = s.warp_sum[warp][lane];
-    const long long own = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long p = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += p;
-    }
-    s.warp_sum[warp][lane] = v - own;
-    if (lane == 31) s.total[warp] = v;
-  }
-  __syncthreads();
-  a = x - a + s.warp_sum[0][warp];
-  b = y - b + s.warp_sum[1][warp];
+  return v;
+}
+template <int kWarps, typename T>
+__device__ __forceinline__ T block_prefix(const T* sums, T& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T v = warp_scan(lane < kWarps ? sums[lane] : T(0));
+  total = __shfl_sync(0xffffffffu, v, kWarps - 1);
+  const T p = __shfl_sync(0xffffffffu, v, (warp + 31) & 31);
+  return warp ? p : T(0);
 }
 
 // Running totals before a chunk.
 struct Carry {
   long long rows = 0, need = 0, released = 0;
-  long long taken = 0;  // pages taken from the head by the sequences that fit
 };
 
-// Decides the chunk of sequences base .. base + 1023 (one per thread) into shared memory.
-__device__ uint32_t decide(const TablesArgs& a, Smem& s, int base, int count, Carry& run, int& new_len) {
-  const int q = base + static_cast<int>(threadIdx.x);
-  const bool in = q < a.n_seq;
-  int c = in ? a.cached[q] : 0;
-  const int n = in ? a.fresh[q] : 0;
+// Decides the chunk of sequences from base on (kPer consecutive ones per thread) into
+// shared memory; ends with a barrier.
+template <int kThreads, int kPer>
+__device__ uint32_t decide(const TablesArgs& a, Smem<kThreads, kPer>& s, int base, int count, Carry& run,
+                           int (&new_len)[kPer]) {
+  constexpr int kWarps = kThreads / 32;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const long long limit = static_cast<long long>(a.max_pages) * kPage;
-  const bool bad = c < 0 || c > limit;
-  uint32_t flags = bad ? KVTC_STATUS_BAD_POS : 0u;
-  if (bad) c = 0;
-  const int held = (c + kPage - 1) / kPage;
-  const bool finished = n < 0;
-  long long row = n > 0 ? n : 0, rel = finished ? held : 0;
-  scan2(s, row, rel);
-  row += run.rows;
-  rel += run.released;
-  run.rows += s.total[0];
-  run.released += s.total[1];
-  __syncthreads();
-  const bool fits = in && !finished && !bad && static_cast<long long>(c) + n <= limit && row + n <= a.n_rows;
-  if (in && n > 0 && !fits) flags |= KVTC_STATUS_BAD_POS;
-  const long long need = fits ? (static_cast<long long>(c) + n + kPage - 1) / kPage - held : 0;
-  long long first = need, unused = 0;
-  scan2(s, first, unused);
-  first += run.need;
-  run.need += s.total[0];
-  const bool grows = fits && (need == 0 || first + need <= count);
-  if (fits && !grows) flags |= KVTC_STATUS_NO_PAGE;
-  const int t = threadIdx.x;
-  s.first_row[t] = static_cast<int>(min(row, static_cast<long long>(a.n_rows)));
-  s.cached[t] = c;
-  s.page0[t] = grows ? static_cast<int>(min(first, static_cast<long long>(count))) : 0;
-  s.need[t] = !in ? -1 : finished ? -2 : grows ? static_cast<int>(need) : -1;
-  s.release0[t] = static_cast<int>(min(rel, static_cast<long long>(a.capacity)));
-  if (t == kThreads - 1) s.first_row[kThreads] = static_cast<int>(min(run.rows, static_cast<long long>(a.n_rows)));
-  new_len = finished ? 0 : grows ? c + n : c;
-  // the sequences that take pages are a prefix of those that need some: the largest end
-  long long end = grows && need > 0 ? first + need : 0;
+  int c[kPer], n[kPer], held[kPer];
+  bool bad[kPer];
+  uint32_t flags = 0;
+  long long row = 0, rel = 0;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) end = max(end, __shfl_xor_sync(0xffffffffu, end, o));
-  __syncthreads();  // the totals have been read
-  if ((t & 31) == 0) s.warp_sum[0][t >> 5] = end;
+  for (int k = 0; k < kPer; ++k) {
+    const int q = base + t * kPer + k;
+    c[k] = q < a.n_seq ? a.cached[q] : 0;
+    n[k] = q < a.n_seq ? a.fresh[q] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    bad[k] = c[k] < 0 || c[k] > limit;
+    if (bad[k]) flags |= KVTC_STATUS_BAD_POS, c[k] = 0;
+    held[k] = (c[k] + kPage - 1) / kPage;
+    row += max(n[k], 0);
+    rel += n[k] < 0 ? held[k] : 0;
+  }
+  const long long row_incl = warp_scan(row), rel_incl = warp_scan(rel);
+  if (lane == 31) s.rows_sum[warp] = row_incl, s.released_sum[warp] = rel_incl;
   __syncthreads();
-  long long most = run.taken;
-  for (int w = 0; w < kWarps; ++w) most = max(most, s.warp_sum[0][w]);
-  run.taken = most;
+  long long rows_total, rel_total;
+  row = run.rows + block_prefix<kWarps>(s.rows_sum, rows_total) + row_incl - row;
+  rel = run.released + block_prefix<kWarps>(s.released_sum, rel_total) + rel_incl - rel;
+  run.rows += rows_total;
+  run.released += rel_total;
+  bool fits[kPer];
+  int need[kPer], first_row[kPer], release0[kPer], all = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int q = base + t * kPer + k, fresh = max(n[k], 0);
+    fits[k] = q < a.n_seq && n[k] >= 0 && !bad[k] && static_cast<long long>(c[k]) + fresh <= limit && row + fresh <= a.n_rows;
+    if (n[k] > 0 && !fits[k]) flags |= KVTC_STATUS_BAD_POS;
+    // below 2^24 pages each, and their rows (so their sum) fit n_rows
+    need[k] = fits[k] ? static_cast<int>((static_cast<long long>(c[k]) + fresh + kPage - 1) / kPage) - held[k] : 0;
+    all += need[k];
+    first_row[k] = static_cast<int>(min(row, static_cast<long long>(a.n_rows)));
+    release0[k] = static_cast<int>(min(rel, static_cast<long long>(a.capacity)));
+    row += fresh;
+    rel += n[k] < 0 ? held[k] : 0;
+  }
+  const int need_incl = warp_scan(all);
+  if (lane == 31) s.need_sum[warp] = need_incl;
+  __syncthreads();
+  int need_total;
+  long long first = run.need + block_prefix<kWarps>(s.need_sum, need_total) + need_incl - all;
+  run.need += need_total;
+  long long taken = 0;  // the sequences that take pages are a prefix of those that need some
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int q = base + t * kPer + k, i = t * kPer + k;
+    const bool grows = fits[k] && (need[k] == 0 || first + need[k] <= count);
+    if (fits[k] && !grows) flags |= KVTC_STATUS_NO_PAGE;
+    if (grows && need[k] > 0) taken = first + need[k];
+    const bool finished = q < a.n_seq && n[k] < 0;
+    s.first_row[i] = first_row[k];
+    s.cached[i] = c[k];
+    s.page0[i] = grows ? static_cast<int>(min(first, static_cast<long long>(count))) : 0;
+    s.need[i] = finished ? -2 : grows ? need[k] : -1;
+    s.release0[i] = release0[k];
+    new_len[k] = finished ? 0 : grows ? c[k] + n[k] : c[k];
+    first += need[k];
+  }
+  const int most = __reduce_max_sync(0xffffffffu, static_cast<int>(taken));  // at most count
+  if (lane == 0 && most > 0) atomicMax(&s.taken, most);
+  if (t == kThreads - 1) s.first_row[kThreads * kPer] = static_cast<int>(min(run.rows, static_cast<long long>(a.n_rows)));
+  __syncthreads();
   return flags;
 }
 
+template <int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) step_tables_kernel(const __grid_constant__ TablesArgs a) {
-  __shared__ Smem s;
+  constexpr int kWarps = kThreads / 32, kChunk = kThreads * kPer, kRowsPerCta = kThreads * kRowsPerThread;
+  __shared__ Smem<kThreads, kPer> s;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (t == 0) s.taken = 0;  // (the scans' barriers come before its first use)
   griddep_wait();
   griddep_launch_dependents();
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   int head = a.state[0], count = a.state[1];
   uint32_t flags = 0;
   if (head < 0 || head >= a.capacity || count < 0 || count > a.capacity) {
@@ -151,15 +181,67 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const __grid_cons
     flags |= KVTC_STATUS_BAD_PAGE;
   }
   const int room = a.capacity - count;  // places a release can fill
-  const int n_chunks = (a.n_seq + kThreads - 1) / kThreads;
+  const int n_chunks = (a.n_seq + kChunk - 1) / kChunk;
   const int row_lo = static_cast<int>(min(static_cast<long long>(blockIdx.x) * kRowsPerCta, static_cast<long long>(a.n_rows)));
   const int row_hi = static_cast<int>(min(static_cast<long long>(row_lo) + kRowsPerCta, static_cast<long long>(a.n_rows)));
+  const bool writes = !a.in_place && blockIdx.x == 0;
   Carry run;
-  int new_len = 0;
+  int new_len[kPer];
+  auto write_lens = [&](int base) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = t * kPer + k;
+      if (base + i < a.n_seq) {
+        a.seq_lens[base + i] = new_len[k];
+        a.cu[base + i] = s.first_row[i];
+      }
+    }
+  };
   for (int ch = 0; ch < n_chunks; ++ch) {
-    const int base = ch * kThreads;
+    const int base = ch * kChunk;
     flags |= decide(a, s, base, count, run, new_len);
-    const int n_in = min(kThreads, a.n_seq - base);
+    if (writes) write_lens(base);
+    const int n_in = min(kChunk, a.n_seq - base);
+    // this CTA's rows that fall into the chunk: all of a thread's at once
+    const int lo = max(row_lo, s.first_row[0]), hi = min(row_hi, s.first_row[kChunk]);
+    int l[kRowsPerThread], h[kRowsPerThread];  // the last sequence whose first row is <= r
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) l[i] = 0, h[i] = n_in - 1;
+    if (lo < hi) {
+      for (int span = n_in - 1; span > 0; span >>= 1)
+#pragma unroll
+        for (int i = 0; i < kRowsPerThread; ++i) {
+          const int r = lo + min(t + i * kThreads, hi - lo - 1), mid = (l[i] + h[i] + 1) >> 1;
+          const bool up = s.first_row[mid] <= r;
+          l[i] = up ? mid : l[i];
+          h[i] = up ? h[i] : max(mid - 1, l[i]);
+        }
+    }
+    int32_t id[kRowsPerThread];
+    int pos[kRowsPerThread];
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      const int off = t + i * kThreads, r = lo + off;
+      id[i] = -1;
+      pos[i] = 0;
+      if (off < hi - lo && s.need[l[i]] >= 0) {
+        const int c = s.cached[l[i]], held = (c + kPage - 1) / kPage;
+        pos[i] = c + (r - s.first_row[l[i]]);
+        const int p = pos[i] / kPage;
+        const long long at = static_cast<long long>(head) + s.page0[l[i]] + (p - held);
+        id[i] = p < held ? a.table[static_cast<size_t>(base + l[i]) * a.max_pages + p]
+                         : a.ring[at < a.capacity ? at : at - a.capacity];
+        if (id[i] < 0) flags |= KVTC_STATUS_BAD_PAGE;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      const int off = t + i * kThreads, r = lo + off;
+      if (off < hi - lo) {
+        a.slots[r] = id[i] < 0 ? -1 : static_cast<int64_t>(id[i]) * kPage + pos[i] % kPage;
+        a.positions[r] = id[i] < 0 ? 0 : pos[i];
+      }
+    }
     // new table entries and released pages: a warp per sequence, dealt over the CTAs
     for (int i = static_cast<int>(blockIdx.x) * kWarps + warp; i < n_in; i += kWarps * static_cast<int>(gridDim.x)) {
       const int c = s.cached[i], need = s.need[i], held = (c + kPage - 1) / kPage;
@@ -181,74 +263,40 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const __grid_cons
         }
       }
     }
-    // this CTA's rows that fall into the chunk
-    const int lo = max(row_lo, s.first_row[0]), hi = min(row_hi, s.first_row[kThreads]);
-    for (int r = lo + t; r < hi; r += kThreads) {
-      int l = 0, h = n_in - 1;  // the last sequence whose first row is <= r
-      while (l < h) {
-        const int mid = (l + h + 1) >> 1;
-        if (s.first_row[mid] <= r)
-          l = mid;
-        else
-          h = mid - 1;
-      }
-      const int c = s.cached[l], held = (c + kPage - 1) / kPage;
-      int64_t slot = -1;
-      int pos = 0;
-      if (s.need[l] >= 0) {
-        pos = c + (r - s.first_row[l]);
-        const int p = pos / kPage;
-        int32_t id;
-        if (p < held) {
-          id = a.table[static_cast<size_t>(base + l) * a.max_pages + p];
-        } else {
-          const long long at = static_cast<long long>(head) + s.page0[l] + (p - held);
-          id = a.ring[at < a.capacity ? at : at - a.capacity];
-        }
-        if (id >= 0)
-          slot = static_cast<int64_t>(id) * kPage + pos % kPage;
-        else
-          flags |= KVTC_STATUS_BAD_PAGE, pos = 0;
-      }
-      a.slots[r] = slot;
-      a.positions[r] = pos;
-    }
     if (n_chunks > 1) __syncthreads();  // the next chunk overwrites the tables
   }
   // rows behind the last sequence's
-  for (int r = max(row_lo, static_cast<int>(min(run.rows, static_cast<long long>(a.n_rows)))) + t; r < row_hi; r += kThreads) {
+  for (long long r = max(static_cast<long long>(row_lo), min(run.rows, static_cast<long long>(a.n_rows))) + t; r < row_hi; r += kThreads) {
     a.slots[r] = -1;
     a.positions[r] = 0;
   }
   if (flags && a.status) atomicOr(a.status, static_cast<int>(flags));
-  // lengths, row prefix and ring state: by the last CTA that has read its inputs
-  if (gridDim.x > 1) {
-    __syncthreads();
-    if (t == 0) {
-      __threadfence();
-      s.last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
-      __threadfence();
+  // lengths, row prefix and ring state that replace inputs: by the last CTA that has read them
+  if (!writes) {
+    if (!a.in_place) return;
+    if (gridDim.x > 1) {
+      __syncthreads();
+      if (t == 0) {
+        __threadfence();
+        s.last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+        __threadfence();
+      }
+      __syncthreads();
+      if (!s.last) return;
+      if (t == 0) *a.ticket = 0;
     }
-    __syncthreads();
-    if (!s.last) return;
-    if (t == 0) *a.ticket = 0;
-  }
-  Carry again;
-  for (int ch = 0; ch < n_chunks; ++ch) {
-    const int base = ch * kThreads;
-    if (n_chunks > 1) (void)decide(a, s, base, count, again, new_len);
-    if (base + t < a.n_seq) {
-      a.seq_lens[base + t] = new_len;
-      a.cu[base + t] = s.first_row[t];
-      if (base + t == a.n_seq - 1)
-        a.cu[a.n_seq] = static_cast<int>(min(run.rows, static_cast<long long>(a.n_rows)));
+    Carry again;
+    for (int ch = 0; ch < n_chunks; ++ch) {
+      if (n_chunks > 1) (void)decide(a, s, ch * kChunk, count, again, new_len);
+      write_lens(ch * kChunk);
+      if (n_chunks > 1) __syncthreads();
     }
-    if (n_chunks > 1) __syncthreads();
   }
   if (t == 0) {
+    a.cu[a.n_seq] = static_cast<int>(min(run.rows, static_cast<long long>(a.n_rows)));
     const int kept = static_cast<int>(min(run.released, static_cast<long long>(room)));
-    a.state_out[0] = static_cast<int>((head + run.taken) % a.capacity);
-    a.state_out[1] = static_cast<int>(count - run.taken + kept);
+    a.state_out[0] = static_cast<int>((static_cast<long long>(head) + s.taken) % a.capacity);
+    a.state_out[1] = static_cast<int>(static_cast<long long>(count) - s.taken + kept);
   }
 }
 
@@ -308,10 +356,15 @@ extern "C" kvtc_status kvtc_step_tables(const int32_t* cached_lens, const int32_
   a.positions = positions;
   a.n_rows = n_rows;
   a.state_out = ring_state_out;
+  a.in_place = seq_lens == cached_lens || ring_state_out == ring_state;
   a.ticket = static_cast<int*>(workspace);
   a.status = status;
-  const unsigned grid = static_cast<unsigned>(std::max<long long>(1, (static_cast<long long>(n_rows) + kRowsPerCta - 1) / kRowsPerCta));
-  const cudaError_t e = raw::launch(step_tables_kernel, dim3(grid), kThreads, 0, stream, a);
+  const bool small = n_seq <= kSmallThreads;
+  const long long per_cta = kRowsPerThread * (small ? kSmallThreads : kLargeThreads);
+  const unsigned grid = static_cast<unsigned>(std::max<long long>(1, (n_rows + per_cta - 1) / per_cta));
+  const cudaError_t e = small ? raw::launch(step_tables_kernel<kSmallThreads, 1>, dim3(grid), kSmallThreads, 0, stream, a)
+                              : raw::launch(step_tables_kernel<kLargeThreads, kLargePer>, dim3(grid), kLargeThreads, 0,
+                                            stream, a);
   if (e != cudaSuccess) return cuda_fail(e, "step tables launch");
   return KVTC_OK;
 }

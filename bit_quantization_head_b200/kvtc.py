@@ -419,20 +419,25 @@ def kvtc_step_tables(cached_lens, new_lens, page_ring, ring_state, block_table, 
     slot map int64).  ring_state_out may be ring_state and seq_lens may be cached_lens."""
     import torch
     i32, dev = torch.int32, _device(cached_lens, "cached_lens")
-    n_seq, rows = cached_lens.numel(), slot_map.numel()
+    n_seq, rows, capacity = cached_lens.numel(), slot_map.numel(), page_ring.numel()
     if block_table.dim() != 2:
         raise ValueError("block_table must have shape [n_seq][max_pages]")
     max_pages = block_table.shape[1]
     if workspace.nbytes < 16:
         raise ValueError("workspace must hold 16 bytes")
-    per_seq = (n_seq,)
+    p = []
+    for t, name, n in ((cached_lens, "cached_lens", n_seq), (new_lens, "new_lens", n_seq),
+                       (page_ring, "page_ring", capacity), (ring_state, "ring_state", 2),
+                       (block_table, "block_table", n_seq * max_pages), (seq_lens, "seq_lens", n_seq),
+                       (cu_seqlens, "cu_seqlens", n_seq + 1), (positions, "positions", rows),
+                       (ring_state_out, "ring_state_out", 2)):
+        if t.get_device() != dev or t.dtype is not i32 or not t.is_contiguous() or t.numel() != n:
+            _buf(t, i32, name, dev)
+            raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+        p.append(t.data_ptr())
     st = lib().kvtc_step_tables(
-        _buf(cached_lens, i32, "cached_lens", dev), _buf(new_lens, i32, "new_lens", dev, per_seq), n_seq,
-        _buf(page_ring, i32, "page_ring", dev), page_ring.numel(), _buf(ring_state, i32, "ring_state", dev, (2,)),
-        _buf(block_table, i32, "block_table", dev, (n_seq, max_pages)), max_pages,
-        _buf(seq_lens, i32, "seq_lens", dev, per_seq), _buf(cu_seqlens, i32, "cu_seqlens", dev, (n_seq + 1,)),
-        _buf(slot_map, torch.int64, "slot_map", dev), _buf(positions, i32, "positions", dev, (rows,)), rows,
-        _buf(ring_state_out, i32, "ring_state_out", dev, (2,)), _buf(workspace, None, "workspace", dev),
+        p[0], p[1], n_seq, p[2], capacity, p[3], p[4], max_pages, p[5], p[6], _buf(slot_map, torch.int64, "slot_map", dev),
+        p[7], rows, p[8], _buf(workspace, None, "workspace", dev),
         None if status is None else _buf(status, i32, "status", dev), _stream_on(dev, stream))
     if st:
         _check(st)
