@@ -83,7 +83,7 @@ struct __align__(1024) Smem {
   unsigned char out[8][32 * 128];  // half of each row warp's output rows
   Part part[2];
   uint64_t kv_full[kStages], kv_empty[kStages], q_full, q_empty, part_full[2], part_empty[2];
-  uint64_t s_full[2], p_full[2][2], o_full[2], join[2], twin_full, twin_empty, drain;
+  uint64_t s_full[2], p_full[2][2], o_full[2], twin_full, twin_empty, drain;
   int dead;
   int arrived[2][2];       // [tile][part & 1]
   float2 twin_ml[kRows];   // the second tile's m and l of a twin part
@@ -279,20 +279,19 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
   const int lane = threadIdx.x & 31;
   volatile int* dead = &s.dead;
   // slots of all sequences and the longest one's steps
-  long long total = 0;
   int longest = 0;
   bool bad_seq = false;
-  Seq sq;
-  for (int i = lane; i < a.n_seq; i += 32) {
-    sq = seq_of(a, i);
-    bad_seq |= sq.bad;
-    total += static_cast<long long>(sq.steps + kUnitCost) * sq.blocks;
-    if (sq.blocks) longest = max(longest, sq.steps);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  auto slots = [&](int i) {
+    const Seq q = seq_of(a, i);
+    return static_cast<long long>(q.steps + kUnitCost) * q.blocks * a.H;
+  };
+  const long long total = sum_slots(a.n_seq, [&](int i) {
+    const Seq q = seq_of(a, i);
+    bad_seq |= q.bad;
+    if (q.blocks) longest = max(longest, q.steps);
+    return static_cast<long long>(q.steps + kUnitCost) * q.blocks * a.H;
+  });
   longest = __reduce_max_sync(0xffffffffu, longest);
-  total *= a.H;
   if (bad_seq && blockIdx.x == 0 && a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_BAD_POS));
   // A run of r steps saves (longest / r) joins of about half a step each at the end of a
   // unit: no run shorter than sqrt(longest / 2).
@@ -303,29 +302,10 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
     f = run_start(blockIdx.x, n_cta, total);
     f1 = run_start(blockIdx.x + 1, n_cta, total);
   }
-  // the sequence of the run's first slot
-  int seq = 0, n_part = 0, n_q = 0, it = 0;
+  int n_part = 0, n_q = 0, it = 0;
   long long base = 0;  // first slot of the sequence's units
-  for (int i0 = 0; f < f1; i0 += 32) {
-    const int i = i0 + lane;
-    if (a.n_seq > 32) sq = seq_of(a, min(i, a.n_seq - 1));
-    const long long mine = i < a.n_seq ? static_cast<long long>(sq.steps + kUnitCost) * sq.blocks * a.H : 0;
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, f < base + incl);  // lanes at or past it
-    if (past) {
-      const int at = __ffs(past) - 1;
-      seq = i0 + at;
-      base += __shfl_sync(0xffffffffu, incl - mine, at);
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  sq = seq_of(a, seq);
+  int seq = f < f1 ? find_slot(a.n_seq, slots, f, base) : 0;
+  Seq sq = seq_of(a, seq);
   uint32_t flags = 0;
   bool ok = true;
   auto load = [&](int row) {  // the 128 rows from `row` into the next stage (lane 0)
@@ -567,23 +547,21 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
   const uint32_t ts = tmem + lanes + x * 128, to = tmem + lanes + 256 + x * 128;
   const int tok_in = row / a.G, head_in = row - tok_in * a.G;
   const uint64_t c2 = pair(a.c, a.c);
-  uint32_t join_phase = 0, twin_phase = 0;
+  uint32_t twin_phase = 0;
   int it = 0, n_s = 0, n_o = 0;
   auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
     const bool ok = wait_warp(bar, phase, dead);
-    if (!ok && lane == 0) {
-      *dead = 1;
-      if (a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_TIMEOUT));
+    if (!ok) {
+      if (lane == 0) {
+        *dead = 1;
+        if (a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_TIMEOUT));
+      }
+      __syncwarp();
+      leave_barrier(1 + x, kRows);
     }
     return ok;
   };
-  // Barrier of the tile's four warps.
-  auto tile_sync = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.join[x]);
-    join_phase ^= 1;
-    return wait(&s.join[x], join_phase ^ 1);
-  };
+  auto tile_sync = [&]() -> bool { return consumers_sync(1 + x, kRows, dead); };  // the tile's four warps
   for (int n = 0;; ++n) {
     if (!wait(&s.part_full[n & 1], (n >> 1) & 1)) return;
     const Part d = s.part[n & 1];
@@ -912,7 +890,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.p_full[i][0], 4);
       mbar_init(&s.p_full[i][1], 4);
       mbar_init(&s.o_full[i], 1);
-      mbar_init(&s.join[i], 4);
     }
     s.dead = 0;
     fence_mbar_init();

@@ -53,22 +53,18 @@ struct TileDesc {
   int seq, head;  // head: h * groups + group
   int c0, c1;  // CTAs that share the unit
 };
-enum { kFirst = 1, kLast = 2, kBad = 4, kBegins = 8, kEnds = 16 };
+enum { kFirst = 1, kLast = 2, kBad = 4, kBegins = 8, kEnds = 16, kRunEnds = 32, kNothing = 64 };
 
 template <int NT>
 struct __align__(1024) Smem {
   unsigned char kv[stages(NT)][kTileBytes];
   unsigned char q[stages(NT)][NT * 8 * 256];
-  float z[8 * kRowPad];
+  float z[2][8 * kRowPad];  // sums of warps 0 + 2 and of warps 1 + 3
   float m[kConsumers][NT * 8], l[kConsumers][NT * 8];
   TileDesc desc[stages(NT)];
   uint64_t full[stages(NT)], empty[stages(NT)];
-  uint64_t join;  // barrier of the consumer warps
-  long long first_tile, total;
-  int first_seq;
   int dead;
   int last;
-  long long warp_sum[kConsumers + 1];
 };
 
 struct DecodeArgs {
@@ -118,13 +114,24 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 }
 // ------------------------------------------------------------------ producer warp
 template <int NT>
-__device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map, long long f, long long f1, int n_cta) {
+__device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map) {
   const int lane = threadIdx.x & 31;
   const int units = a.H * a.groups;
   volatile int* dead = &s.dead;
-  int seq = s.first_seq, it = 0;
-  long long base = s.first_tile;  // first tile of the sequence's units
   bool bad_len;
+  // the run: tiles f .. f1 - 1 of all units' in a row
+  auto tiles = [&](int i) { return static_cast<long long>(n_tiles(seq_len(a, i, bad_len))) * units; };
+  const long long total = sum_slots(a.n_seq, tiles);
+  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), total));  // no CTA without a tile
+  long long f = 0, f1 = 0, base = 0;  // base: first tile of the sequence's units
+  if (static_cast<int>(blockIdx.x) < n_cta) {
+    f = run_start(blockIdx.x, n_cta, total);
+    f1 = run_start(blockIdx.x + 1, n_cta, total);
+  } else if (lane == 0) {
+    s.desc[0].flags = kNothing;
+    mbar_arrive(&s.full[0]);
+  }
+  int seq = f < f1 ? find_slot(a.n_seq, tiles, f, base) : 0, it = 0;
   int len = seq_len(a, seq, bad_len), nt = n_tiles(len);
   int page0 = -1, page_id = -1, page_seq = -1;  // 32 page ids from page0 on, one per lane
   bool ok = true;
@@ -137,11 +144,11 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
       nt = n_tiles(len);
     }
     if (bad_len) flags_seen |= KVTC_STATUS_BAD_POS;
-    const int u = static_cast<int>((f - base) / nt);
+    const int u = static_cast<int>(divide(f - base, nt));
     const int i0 = static_cast<int>(f - base - static_cast<long long>(u) * nt);
     const int i1 = static_cast<int>(min(static_cast<long long>(nt), i0 + (f1 - f)));
     const long long begin = base + static_cast<long long>(u) * nt;
-    const int c0 = run_owner(begin, n_cta, s.total), c1 = run_owner(begin + nt - 1, n_cta, s.total);
+    const int c0 = run_owner(begin, n_cta, total), c1 = run_owner(begin + nt - 1, n_cta, total);
     const int h = u / a.groups, grp = u - h * a.groups;
     const int heads = min(a.group_heads, a.G - grp * a.group_heads);
     for (int i = i0; i < i1 && ok; ++i, ++it) {
@@ -162,7 +169,8 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
           TileDesc& d = s.desc[st];
           d.n = good ? min(kTile, len - i * kTile) : 0;
           d.flags = (i == i0 ? kFirst : 0) | (i == i1 - 1 ? kLast : 0) | (have && !good ? kBad : 0) |
-                    (i0 == 0 ? kBegins : 0) | (i1 == nt ? kEnds : 0);
+                    (i0 == 0 ? kBegins : 0) | (i1 == nt ? kEnds : 0) |
+                    (i == i1 - 1 && f + (i1 - i0) == f1 ? kRunEnds : 0);
           d.seq = seq;
           d.head = u;
           d.c0 = c0;
@@ -220,7 +228,7 @@ __device__ __forceinline__ float* part_of(const DecodeArgs& a, int c, int slot) 
 }
 
 template <int NT, bool F16>
-__device__ void consume(const DecodeArgs& a, Smem<NT>& s, int n_iter) {
+__device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   volatile int* dead = &s.dead;
@@ -233,31 +241,20 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s, int n_iter) {
   uint32_t qf[NT][8][2];
   float z[NT][8][4], m[NT][2], l[NT][2];
   bool bad = false;
-  uint32_t join_phase = 0;
-  // Gives up for the whole CTA: the other roles see it in their next wait.
-  auto give_up = [&] {
-    if (lane == 0) {
-      *dead = 1;
-      if (a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_TIMEOUT));
-    }
-  };
-  // Barrier of the consumer warps; false (in the whole warp) if the CTA gave up.
-  auto consumer_sync = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.join);
-    const bool ok = __all_sync(0xffffffffu, wait_phase(&s.join, join_phase, dead));
-    join_phase ^= 1;
-    if (!ok) give_up();
-    return ok;
-  };
-  for (int it = 0; it < n_iter; ++it) {
+  auto consumer_sync = [&]() -> bool { return consumers_sync(1, 32 * kConsumers, dead); };
+  for (int it = 0;; ++it) {
     const int st = it % stages(NT);
-    const bool ok = wait_phase(&s.full[st], (it / stages(NT)) & 1, dead);
-    if (!__all_sync(0xffffffffu, ok)) {
-      give_up();
+    if (!wait_warp(&s.full[st], (it / stages(NT)) & 1, dead)) {
+      if (lane == 0) {
+        *dead = 1;
+        if (a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_TIMEOUT));
+      }
+      __syncwarp();
+      leave_barrier(1, 32 * kConsumers);
       return;
     }
     const TileDesc d = s.desc[st];
+    if (d.flags & kNothing) return;
     const int h = d.head / a.groups, grp = d.head - h * a.groups;
     const int heads = min(a.group_heads, a.G - grp * a.group_heads);
     if (d.flags & kFirst) {
@@ -377,13 +374,15 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s, int n_iter) {
         const float top = fmaxf(fmaxf(s.m[0][hd], s.m[1][hd]), fmaxf(s.m[2][hd], s.m[3][hd]));
         f[j] = m[n][j] == -INFINITY ? 0.0f : ex2((m[n][j] - top) * a.c);
       }
-      for (int w = 0; w < kConsumers; ++w) {  // in warp order
-        if (warp == w) {
+      // (z0 + z2) + (z1 + z3), whatever the warps' order
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (warp >> 1 == w) {
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float* p = s.z + (2 * t + (e & 1)) * kRowPad + 16 * mt + (e >> 1) * 8 + g;
+              float* p = s.z[warp & 1] + (2 * t + (e & 1)) * kRowPad + 16 * mt + (e >> 1) * 8 + g;
               const float v = z[n][mt][e] * f[e & 1];
               *p = w == 0 ? v : *p + v;
             }
@@ -401,7 +400,7 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s, int n_iter) {
           sum += s.m[w][row] == -INFINITY ? 0.0f : s.l[w][row] * ex2((s.m[w][row] - top) * a.c);
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = s.z[hd * kRowPad + dim + e];
+        for (int e = 0; e < 8; ++e) v[e] = s.z[0][hd * kRowPad + dim + e] + s.z[1][hd * kRowPad + dim + e];
         if (whole) {
           if (bad) {
 #pragma unroll
@@ -420,43 +419,90 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s, int n_iter) {
       }
       if (!consumer_sync()) return;
     }
-    if (whole) continue;
+    if (whole) {
+      if (d.flags & kRunEnds) return;
+      continue;
+    }
     // ---- the unit is shared with other CTAs: the last one to arrive joins the partials
     __threadfence();
     if (!consumer_sync()) return;
     if (tid == 0) s.last = atomicAdd(a.tickets + d.c0, 1) == d.c1 - d.c0;
     if (!consumer_sync()) return;
-    if (!s.last) continue;
+    if (!s.last) {
+      if (d.flags & kRunEnds) return;
+      continue;
+    }
     __threadfence();
-    for (int n = 0; n < NT; ++n) {
-      const int row = n * 8 + (tid >> 4), dim = (tid & 15) * 8;
-      if (row >= heads) continue;
+    const int n_part = d.c1 - d.c0 + 1;
+    for (int n = 0; n < NT && n * 8 < heads; ++n) {
+      // the largest reference of each head: 16 parts at a time
       float top = -INFINITY;
       bool any_bad = false;
-      for (int c = d.c0; c <= d.c1; ++c) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of<NT>(a, c, c == d.c0) + NT * 8 * kD + 2 * row));
-        top = fmaxf(top, ml.x);
-        any_bad |= ml.y < 0.0f;
+#pragma unroll 4
+      for (int i = tid >> 3; i < n_part; i += 16) {
+        const int c = d.c0 + i;
+        if (n * 8 + (tid & 7) < heads) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of<NT>(a, c, c == d.c0) + NT * 8 * kD + 2 * (n * 8 + (tid & 7))));
+          top = fmaxf(top, ml.x);
+          any_bad |= ml.y < 0.0f;
+        }
       }
+      s.z[0][tid] = top;
+      s.z[1][tid] = any_bad ? 1.0f : 0.0f;
+      if (!consumer_sync()) return;
+      // a head's 16 chunks of 8 dims by 16 threads; with at most 4 heads the parts are dealt
+      // over the threads left (their sums are added in order)
+      const int live = min(8, heads - n * 8), deal = live <= 1 ? 8 : live <= 2 ? 4 : live <= 4 ? 2 : 1, own = 8 / deal;
+      const int slot = tid >> 4, hd = slot % own, sub = slot / own, row = n * 8 + hd, dim = (tid & 15) * 8;
       float v[8] = {}, sum = 0.0f;
-#pragma unroll 8
-      for (int c = d.c0; c <= d.c1; ++c) {
-        const float* p = part_of<NT>(a, c, c == d.c0);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + NT * 8 * kD + 2 * row));
-        const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim) + 0);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim) + 1);
-        sum += ml.y * f;
-        v[0] += x.x * f, v[1] += x.y * f, v[2] += x.z * f, v[3] += x.w * f;
-        v[4] += y.x * f, v[5] += y.y * f, v[6] += y.z * f, v[7] += y.w * f;
-      }
-      if (any_bad) {
+      top = -INFINITY;
+      any_bad = false;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+      for (int i = 0; i < 16; ++i) {
+        top = fmaxf(top, s.z[0][8 * i + hd]);
+        any_bad |= s.z[1][8 * i + hd] != 0.0f;
       }
-      store_out<F16>(a.out + (out0 + row) * kD + dim, v, any_bad ? 0.0f : sum);
+      if (hd < live) {
+#pragma unroll 8
+        for (int i = sub; i < n_part; i += deal) {
+          const int c = d.c0 + i;
+          const float* p = part_of<NT>(a, c, c == d.c0);
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + NT * 8 * kD + 2 * row));
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim));
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim) + 1);
+          const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
+          sum += ml.y * f;
+          v[0] += x.x * f, v[1] += x.y * f, v[2] += x.z * f, v[3] += x.w * f;
+          v[4] += y.x * f, v[5] += y.y * f, v[6] += y.z * f, v[7] += y.w * f;
+        }
+      }
+      if (!consumer_sync()) return;
+      if (deal > 1) {
+        float* mine = s.z[0] + slot * kRowPad + dim;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine[e] = v[e];
+        if ((tid & 15) == 0) s.z[1][slot] = sum;
+        if (!consumer_sync()) return;
+        if (sub == 0) {
+          for (int k = 1; k < deal; ++k) {
+            const int from = hd + k * own;
+            sum += s.z[1][from];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += s.z[0][from * kRowPad + dim + e];
+          }
+        }
+      }
+      if (sub == 0 && hd < live) {
+        if (any_bad) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        }
+        store_out<F16>(a.out + (out0 + row) * kD + dim, v, any_bad ? 0.0f : sum);
+      }
+      if (!consumer_sync()) return;
     }
     if (tid == 0) a.tickets[d.c0] = 0;
+    if (d.flags & kRunEnds) return;
   }
 }
 
@@ -465,62 +511,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
     raw_decode_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ DecodeArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem<NT>& s = *reinterpret_cast<Smem<NT>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 32 * kConsumers) prefetch_map(&map);
   if (tid == 0) {
     for (int i = 0; i < stages(NT); ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], kConsumers);
     }
-    mbar_init(&s.join, kConsumers);
     s.dead = 0;
     fence_mbar_init();
   }
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  // tiles of all sequences (thread i: the i-th run of them), and the sequence of this CTA's
-  // first tile
-  const int units = a.H * a.groups;
-  const int per = (a.n_seq + kThreads - 1) / kThreads;
-  const int s0 = min(a.n_seq, tid * per), s1 = min(a.n_seq, s0 + per);
-  long long mine = 0;
-  bool bad;
-  for (int i = s0; i < s1; ++i) mine += n_tiles(seq_len(a, i, bad));
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s.warp_sum[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-  for (int w = 0; w <= kConsumers; ++w) {
-    if (w < warp) before += s.warp_sum[w];
-    total += s.warp_sum[w];
-  }
-  total *= units;
-  before *= units;
-  // no CTA without a tile
-  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-  const long long f0 = run_start(blockIdx.x, n_cta, total), f1 = run_start(blockIdx.x + 1, n_cta, total);
-  if (static_cast<int>(blockIdx.x) >= n_cta) return;  // the whole CTA
-  if (before <= f0 && f0 < before + mine * units) {
-    long long b = before;
-    int i = s0;
-    for (; i < s1 - 1; ++i) {
-      const long long n = static_cast<long long>(n_tiles(seq_len(a, i, bad))) * units;
-      if (f0 < b + n) break;
-      b += n;
-    }
-    s.first_seq = i;
-    s.first_tile = b;
-    s.total = total;
-  }
-  __syncthreads();
   if (warp == kConsumers)
-    produce<NT>(a, s, &map, f0, f1, n_cta);
+    produce<NT>(a, s, &map);
   else
-    consume<NT, F16>(a, s, static_cast<int>(f1 - f0));
+    consume<NT, F16>(a, s);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

@@ -22,6 +22,55 @@ __device__ __forceinline__ int run_owner(long long t, long long n, long long tot
   return static_cast<int>(divide((t + 1) * n + total - 1, total)) - 1;
 }
 
+// Sum of slots(i) over the sequences, in every lane of a warp.
+template <typename Slots>
+__device__ __forceinline__ long long sum_slots(int n_seq, const Slots& slots) {
+  long long total = 0;
+  for (int i = threadIdx.x & 31; i < n_seq; i += 32) total += slots(i);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  return total;
+}
+// The sequence that holds slot f (0 <= f < total), by a whole warp; base: its first slot.
+template <typename Slots>
+__device__ __forceinline__ int find_slot(int n_seq, const Slots& slots, long long f, long long& base) {
+  const int lane = threadIdx.x & 31;
+  base = 0;
+  for (int i0 = 0; i0 < n_seq; i0 += 32) {
+    const int i = i0 + lane;
+    const long long mine = i < n_seq ? slots(i) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, f < base + incl);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      base += __shfl_sync(0xffffffffu, incl - mine, at);
+      return i0 + at;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return 0;
+}
+
+// Named barrier of the `threads` threads that consume together, without an endless wait: a
+// warp that leaves because the CTA gave up (the dead flag: a bounded wait ran out) arrives
+// once in its place.  That completes the barrier the others may be in or come to next; the
+// flag was set before it, so each of them sees it there and leaves the same way.
+__device__ __forceinline__ void leave_barrier(int id, int threads) {
+  __threadfence_block();
+  asm volatile("bar.arrive %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool consumers_sync(int id, int threads, volatile int* dead) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+  if (!__any_sync(0xffffffffu, *dead)) return true;
+  leave_barrier(id, threads);
+  return false;
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
