@@ -283,14 +283,12 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
   bool bad_seq = false;
   auto slots = [&](int i) {
     const Seq q = seq_of(a, i);
-    return static_cast<long long>(q.steps + kUnitCost) * q.blocks * a.H;
-  };
-  const long long total = sum_slots(a.n_seq, [&](int i) {
-    const Seq q = seq_of(a, i);
     bad_seq |= q.bad;
     if (q.blocks) longest = max(longest, q.steps);
     return static_cast<long long>(q.steps + kUnitCost) * q.blocks * a.H;
-  });
+  };
+  SlotScan<decltype(slots)> scan(a.n_seq, slots);
+  const long long total = scan.total;
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (bad_seq && blockIdx.x == 0 && a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_BAD_POS));
   // Runs of r steps take r steps and join up to longest / r parts at the end of a unit, a
@@ -305,7 +303,7 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
   }
   int n_part = 0, n_q = 0, it = 0;
   long long base = 0;  // first slot of the sequence's units
-  int seq = f < f1 ? find_slot(a.n_seq, slots, f, base) : 0;
+  int seq = f < f1 ? scan.find(f, base) : 0;
   Seq sq = seq_of(a, seq);
   uint32_t flags = 0;
   bool ok = true;

@@ -120,9 +120,18 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
   volatile int* dead = &s.dead;
   bool bad_len;
   // the run: tiles f .. f1 - 1 of all units' in a row
-  auto tiles = [&](int i) { return static_cast<long long>(n_tiles(seq_len(a, i, bad_len))) * units; };
-  const long long total = sum_slots(a.n_seq, tiles);
-  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), total));  // no CTA without a tile
+  int longest = 0;
+  auto tiles = [&](int i) {
+    const int n = n_tiles(seq_len(a, i, bad_len));
+    longest = max(longest, n);
+    return static_cast<long long>(n) * units;
+  };
+  SlotScan<decltype(tiles)> scan(a.n_seq, tiles);
+  const long long total = scan.total;
+  // Runs of at least 1 to 4 tiles: fewer parts to join where one sequence has the chip (4096
+  // tokens of 8 heads: 11.4 us with 4, 12.8 with 1; 1000 tokens: 9.5 with 1, 10.9 with 2).
+  const int shortest = min(4, max(1, __reduce_max_sync(0xffffffffu, longest) / 16));
+  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), divide(total + shortest - 1, shortest)));
   long long f = 0, f1 = 0, base = 0;  // base: first tile of the sequence's units
   if (static_cast<int>(blockIdx.x) < n_cta) {
     f = run_start(blockIdx.x, n_cta, total);
@@ -131,7 +140,7 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
     s.desc[0].flags = kNothing;
     mbar_arrive(&s.full[0]);
   }
-  int seq = f < f1 ? find_slot(a.n_seq, tiles, f, base) : 0, it = 0;
+  int seq = f < f1 ? scan.find(f, base) : 0, it = 0;
   int len = seq_len(a, seq, bad_len), nt = n_tiles(len);
   int page0 = -1, page_id = -1, page_seq = -1;  // 32 page ids from page0 on, one per lane
   bool ok = true;
@@ -225,6 +234,114 @@ __device__ __forceinline__ void store_out(uint16_t* dst, const float (&z)[8], fl
 template <int NT>
 __device__ __forceinline__ float* part_of(const DecodeArgs& a, int c, int slot) {
   return a.parts + (static_cast<size_t>(c) * 2 + slot) * (NT * 8 * (kD + 2));
+}
+
+// Arrives at `ticket` for this CTA's part; the last of n_part CTAs joins their parts (CTAs
+// first, first + step, ..; c0: the one where the unit begins) into the output, or into the
+// place of the first one's.  False if the CTA gave up; s.last: whether this CTA joined.
+template <int NT, bool F16, bool kFinal>
+__device__ __forceinline__ bool join_parts(const DecodeArgs& a, Smem<NT>& s, int* ticket, int c0, int first, int step,
+                                           int n_part, int heads, size_t out0) {
+  const int tid = threadIdx.x;
+  auto sync = [&]() -> bool { return consumers_sync(1, 32 * kConsumers, &s.dead); };
+  __threadfence();
+  if (!sync()) return false;
+  if (tid == 0) s.last = atomicAdd(ticket, 1) == n_part - 1;
+  if (!sync()) return false;
+  if (!s.last) return true;
+  __threadfence();
+  if (tid == 0) *ticket = 0;
+  for (int n = 0; n < NT && n * 8 < heads; ++n) {
+    // the largest reference of each head: 16 parts at a time
+    float top = -INFINITY;
+    bool any_bad = false;
+#pragma unroll 4
+    for (int i = tid >> 3; i < n_part; i += 16) {
+      const int c = first + i * step;
+      if (n * 8 + (tid & 7) < heads) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of<NT>(a, c, c == c0) + NT * 8 * kD + 2 * (n * 8 + (tid & 7))));
+        top = fmaxf(top, ml.x);
+        any_bad |= ml.y < 0.0f;
+      }
+    }
+    s.z[0][tid] = top;
+    s.z[1][tid] = any_bad ? 1.0f : 0.0f;
+    if (!sync()) return false;
+    // a head's 16 chunks of 8 dims by 16 threads; with at most 4 heads the parts are dealt
+    // over the threads left (their sums are added in order)
+    const int live = min(8, heads - n * 8), deal = live <= 1 ? 8 : live <= 2 ? 4 : live <= 4 ? 2 : 1, own = 8 / deal;
+    const int slot = tid >> 4, hd = slot % own, sub = slot / own, row = n * 8 + hd, dim = (tid & 15) * 8;
+    float v[8] = {}, sum = 0.0f;
+    top = -INFINITY;
+    any_bad = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      top = fmaxf(top, s.z[0][8 * i + hd]);
+      any_bad |= s.z[1][8 * i + hd] != 0.0f;
+    }
+    if (hd < live) {
+#pragma unroll 8
+      for (int i = sub; i < n_part; i += deal) {
+        const int c = first + i * step;
+        const float* p = part_of<NT>(a, c, c == c0);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + NT * 8 * kD + 2 * row));
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim));
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim) + 1);
+        const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
+        sum += ml.y * f;
+        v[0] += x.x * f, v[1] += x.y * f, v[2] += x.z * f, v[3] += x.w * f;
+        v[4] += y.x * f, v[5] += y.y * f, v[6] += y.z * f, v[7] += y.w * f;
+      }
+    }
+    if (!sync()) return false;
+    if (deal > 1) {
+      float* mine = s.z[0] + slot * kRowPad + dim;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mine[e] = v[e];
+      if ((tid & 15) == 0) s.z[1][slot] = sum;
+      if (!sync()) return false;
+      if (sub == 0) {
+        for (int k = 1; k < deal; ++k) {
+          const int from = hd + k * own;
+          sum += s.z[1][from];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += s.z[0][from * kRowPad + dim + e];
+        }
+      }
+    }
+    if (sub == 0 && hd < live) {
+      if (any_bad) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+      }
+      if (kFinal) {
+        store_out<F16>(a.out + (out0 + row) * kD + dim, v, any_bad ? 0.0f : sum);
+      } else {
+        float* p = part_of<NT>(a, first, first == c0);
+        reinterpret_cast<float4*>(p + row * kD + dim)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p + row * kD + dim)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (dim == 0) {
+          p[NT * 8 * kD + 2 * row] = top;
+          p[NT * 8 * kD + 2 * row + 1] = any_bad ? -1.0f : sum;
+        }
+      }
+    }
+    if (!sync()) return false;
+  }
+  return true;
+}
+
+// The same in two levels: groups of CTAs, then the groups' parts.
+template <int NT, bool F16>
+__device__ __noinline__ bool join_groups(const DecodeArgs& a, Smem<NT>& s, int c0, int shares, int heads, size_t out0) {
+  const int group = shares <= 128 ? 8 : 16;
+  const int begin = (static_cast<int>(blockIdx.x) - c0) / group * group, first = c0 + begin;
+  if (!join_parts<NT, F16, false>(a, s, a.tickets + 2 * first + (begin == 0), c0, first, 1, min(group, shares - begin),
+                                  heads, out0))
+    return false;
+  if (!s.last) return true;
+  return join_parts<NT, F16, true>(a, s, a.tickets + 2 * kMaxCtas + c0, c0, c0, group, (shares + group - 1) / group, heads,
+                                   out0);
 }
 
 template <int NT, bool F16>
@@ -323,8 +440,11 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
           m[n][0] = m0;
           m[n][1] = m1;
         }
-        const float p0 = ex2((sc[n][0] - m[n][0]) * a.c), p1 = ex2((sc[n][1] - m[n][1]) * a.c);
-        const float p2 = ex2((sc[n][2] - m[n][0]) * a.c), p3 = ex2((sc[n][3] - m[n][1]) * a.c);
+        // fp16 weights are 2^15 at the maximum, so those far below it keep clear of the
+        // subnormals
+        constexpr float kBias = F16 ? 15.0f : 0.0f;
+        const float p0 = ex2(fmaf(sc[n][0] - m[n][0], a.c, kBias)), p1 = ex2(fmaf(sc[n][1] - m[n][1], a.c, kBias));
+        const float p2 = ex2(fmaf(sc[n][2] - m[n][0], a.c, kBias)), p3 = ex2(fmaf(sc[n][3] - m[n][1], a.c, kBias));
         l[n][0] += p0 + p2;
         l[n][1] += p1 + p3;
         // P enters the value MMA in the pages' type (half a step of relative error on each
@@ -423,86 +543,16 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
       if (d.flags & kRunEnds) return;
       continue;
     }
-    // ---- the unit is shared with other CTAs: the last one to arrive joins the partials
-    __threadfence();
-    if (!consumer_sync()) return;
-    if (tid == 0) s.last = atomicAdd(a.tickets + d.c0, 1) == d.c1 - d.c0;
-    if (!consumer_sync()) return;
-    if (!s.last) {
-      if (d.flags & kRunEnds) return;
-      continue;
-    }
-    __threadfence();
-    const int n_part = d.c1 - d.c0 + 1;
-    for (int n = 0; n < NT && n * 8 < heads; ++n) {
-      // the largest reference of each head: 16 parts at a time
-      float top = -INFINITY;
-      bool any_bad = false;
-#pragma unroll 4
-      for (int i = tid >> 3; i < n_part; i += 16) {
-        const int c = d.c0 + i;
-        if (n * 8 + (tid & 7) < heads) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of<NT>(a, c, c == d.c0) + NT * 8 * kD + 2 * (n * 8 + (tid & 7))));
-          top = fmaxf(top, ml.x);
-          any_bad |= ml.y < 0.0f;
-        }
-      }
-      s.z[0][tid] = top;
-      s.z[1][tid] = any_bad ? 1.0f : 0.0f;
-      if (!consumer_sync()) return;
-      // a head's 16 chunks of 8 dims by 16 threads; with at most 4 heads the parts are dealt
-      // over the threads left (their sums are added in order)
-      const int live = min(8, heads - n * 8), deal = live <= 1 ? 8 : live <= 2 ? 4 : live <= 4 ? 2 : 1, own = 8 / deal;
-      const int slot = tid >> 4, hd = slot % own, sub = slot / own, row = n * 8 + hd, dim = (tid & 15) * 8;
-      float v[8] = {}, sum = 0.0f;
-      top = -INFINITY;
-      any_bad = false;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        top = fmaxf(top, s.z[0][8 * i + hd]);
-        any_bad |= s.z[1][8 * i + hd] != 0.0f;
-      }
-      if (hd < live) {
-#pragma unroll 8
-        for (int i = sub; i < n_part; i += deal) {
-          const int c = d.c0 + i;
-          const float* p = part_of<NT>(a, c, c == d.c0);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + NT * 8 * kD + 2 * row));
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim));
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim) + 1);
-          const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
-          sum += ml.y * f;
-          v[0] += x.x * f, v[1] += x.y * f, v[2] += x.z * f, v[3] += x.w * f;
-          v[4] += y.x * f, v[5] += y.y * f, v[6] += y.z * f, v[7] += y.w * f;
-        }
-      }
-      if (!consumer_sync()) return;
-      if (deal > 1) {
-        float* mine = s.z[0] + slot * kRowPad + dim;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mine[e] = v[e];
-        if ((tid & 15) == 0) s.z[1][slot] = sum;
-        if (!consumer_sync()) return;
-        if (sub == 0) {
-          for (int k = 1; k < deal; ++k) {
-            const int from = hd + k * own;
-            sum += s.z[1][from];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += s.z[0][from * kRowPad + dim + e];
-          }
-        }
-      }
-      if (sub == 0 && hd < live) {
-        if (any_bad) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        }
-        store_out<F16>(a.out + (out0 + row) * kD + dim, v, any_bad ? 0.0f : sum);
-      }
-      if (!consumer_sync()) return;
-    }
-    if (tid == 0) a.tickets[d.c0] = 0;
-    if (d.flags & kRunEnds) return;
+    // ---- the unit is shared with other CTAs: the last one to arrive joins the partials; of
+    // many, groups of CTAs first (74 parts read one after another took 13 us at the end of a
+    // call; groups are joined while other CTAs still compute, and cost 2 us of their own)
+    const int shares = d.c1 - d.c0 + 1;
+    bool ok;
+    if (shares <= 48)
+      ok = join_parts<NT, F16, true>(a, s, a.tickets + 2 * d.c0 + 1, d.c0, d.c0, 1, shares, heads, out0);
+    else
+      ok = join_groups<NT, F16>(a, s, d.c0, shares, heads, out0);
+    if (!ok || (d.flags & kRunEnds)) return;
   }
 }
 
@@ -599,7 +649,8 @@ kvtc_status query_map(CUtensorMap* m, const void* q, kvtc_dtype dtype, int n_tok
 
 using namespace kvtc;
 
-// Counters of the CTAs (4096 bytes), then two partial slots for each.
+// Counters (4096 bytes: two per CTA for the groups of a unit's parts, one for the groups
+// themselves), then two partial slots for each CTA.
 extern "C" uint64_t kvtc_raw_decode_workspace_bytes(int n_seq, int n_q_heads, int n_kv_heads, int max_seq_len) {
   if (n_seq < 1 || n_kv_heads < 1 || n_q_heads < n_kv_heads || max_seq_len < 0) return 0;
   const uint64_t rows = 8ull * raw::n_col_tiles(n_q_heads / n_kv_heads);

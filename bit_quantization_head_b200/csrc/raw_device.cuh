@@ -22,39 +22,56 @@ __device__ __forceinline__ int run_owner(long long t, long long n, long long tot
   return static_cast<int>(divide((t + 1) * n + total - 1, total)) - 1;
 }
 
-// Sum of slots(i) over the sequences, in every lane of a warp.
+// The sequences' slots in a row, by a whole warp: their total, and the sequence that holds a
+// slot.  Up to 32 sequences are read once.
 template <typename Slots>
-__device__ __forceinline__ long long sum_slots(int n_seq, const Slots& slots) {
-  long long total = 0;
-  for (int i = threadIdx.x & 31; i < n_seq; i += 32) total += slots(i);
+struct SlotScan {
+  int n_seq;
+  const Slots& slots;
+  long long total, mine, incl;  // incl: the sum up to the lane's sequence (of the first 32)
+
+  __device__ __forceinline__ SlotScan(int n, const Slots& f) : n_seq(n), slots(f) {
+    const int lane = threadIdx.x & 31;
+    mine = lane < n ? f(lane) : 0;
+    scan();
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    if (n > 32) {
+      long long more = 0;
+      for (int i = lane + 32; i < n; i += 32) more += f(i);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  return total;
-}
-// The sequence that holds slot f (0 <= f < total), by a whole warp; base: its first slot.
-template <typename Slots>
-__device__ __forceinline__ int find_slot(int n_seq, const Slots& slots, long long f, long long& base) {
-  const int lane = threadIdx.x & 31;
-  base = 0;
-  for (int i0 = 0; i0 < n_seq; i0 += 32) {
-    const int i = i0 + lane;
-    const long long mine = i < n_seq ? slots(i) : 0;
-    long long incl = mine;
+      for (int o = 16; o; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+      total += more;
+    }
+  }
+  __device__ __forceinline__ void scan() {
+    const int lane = threadIdx.x & 31;
+    incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, f < base + incl);
-    if (past) {
-      const int at = __ffs(past) - 1;
-      base += __shfl_sync(0xffffffffu, incl - mine, at);
-      return i0 + at;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return 0;
-}
+  // The sequence that holds slot f (0 <= f < total); base: its first slot.
+  __device__ __forceinline__ int find(long long f, long long& base) {
+    const int lane = threadIdx.x & 31;
+    base = 0;
+    for (int i0 = 0; i0 < n_seq; i0 += 32) {
+      if (i0) {
+        mine = i0 + lane < n_seq ? slots(i0 + lane) : 0;
+        scan();
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, f < base + incl);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        base += __shfl_sync(0xffffffffu, incl - mine, at);
+        return i0 + at;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return 0;
+  }
+};
 
 // Named barrier of the `threads` threads that consume together, without an endless wait: a
 // warp that leaves because the CTA gave up (the dead flag: a bounded wait ran out) arrives
