@@ -46,8 +46,8 @@ constexpr int kMaxCtas = 160;                    // partial slots in the workspa
 constexpr int kPartFloats = kRows * (kD + 2);    // (m, l) of each row, then its sums
 constexpr uint32_t kTmemCols = 512;              // S_a, S_b, O_a, O_b
 // Registers of a thread: 384 threads start with 168 each (64512); the row warps take what
-// the others leave (2 * 216 + 72 = 3 * 168).
-constexpr int kRowRegs = 216, kOtherRegs = 72;
+// the others leave (2 * 208 + 88 = 3 * 168).
+constexpr int kRowRegs = 208, kOtherRegs = 88;
 // What a unit costs beside its steps (filling the pipeline, output or parts), in steps: the
 // runs are cut by steps + kUnitCost slots a unit, the first kUnitCost of them without a step.
 constexpr int kUnitCost = 3;
@@ -343,29 +343,31 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
     good = __all_sync(0xffffffffu, good);
     if (!good) flags |= KVTC_STATUS_BAD_PAGE;
     const int steps = good && sq.len > 0 ? i1 - i0 : 0;
-    Part d;
-    d.steps = steps;
-    d.tail = sq.len - (sq.steps - 1) * kPage;
-    d.tok0 = sq.tok0 + blk * 2 * a.tile_tok;
-    d.tok1 = min(sq.tok1, d.tok0 + 2 * a.tile_tok);
-    d.head = h;
-    d.two = d.tok1 - d.tok0 > a.tile_tok;
-    d.twin = !d.two && sq.steps >= kTwinSteps;
-    d.first = i0 == 0;
-    d.last = i1 == sq.steps;
-    d.bad = !good;
-    d.c0 = run_owner(begin, n_cta, total);
-    d.c1 = run_owner(begin + sq.steps - 1, n_cta, total);
-    d.end = f1 - f <= kUnitCost;  // no step of the next unit
-    if (d.end) f = f1;
-    if (lane == 0) {
+    const int tok0 = sq.tok0 + blk * 2 * a.tile_tok, tok1 = min(sq.tok1, tok0 + 2 * a.tile_tok);
+    const int two = tok1 - tok0 > a.tile_tok;
+    if (f1 - f <= kUnitCost) f = f1;  // no step of the next unit
+    auto post = [&] {  // tells the other roles of the part (lane 0)
+      Part d;
+      d.steps = steps;
+      d.tail = sq.len - (sq.steps - 1) * kPage;
+      d.tok0 = tok0;
+      d.tok1 = tok1;
+      d.head = h;
+      d.two = two;
+      d.twin = !two && sq.steps >= kTwinSteps;
+      d.first = i0 == 0;
+      d.last = i1 == sq.steps;
+      d.bad = !good;
+      d.c0 = run_owner(begin, n_cta, total);
+      d.c1 = run_owner(begin + sq.steps - 1, n_cta, total);
+      d.end = f == f1;
       if (n_part >= 2) ok = wait_phase(&s.part_empty[n_part & 1], ((n_part >> 1) - 1) & 1, dead);
       if (ok) {
         s.part[n_part & 1] = d;
         mbar_arrive(&s.part_full[n_part & 1]);
       }
-    }
-    ++n_part;
+    };
+    if (steps == 0 && lane == 0) post();
     for (int i = i0; i < i0 + steps; ++i) {
       if (i > i0 && ((i - i0) & 31) == 0) ids = i + lane < i1 ? pages[i + lane] : 0;
       const int id = __shfl_sync(0xffffffffu, ids, (i - i0) & 31);
@@ -376,17 +378,19 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
           if (n_q > 0) ok = wait_phase(&s.q_empty, (n_q - 1) & 1, dead);
           if (ok) {
             const uint32_t bytes = static_cast<uint32_t>(a.tile_tok * a.G) * 128u;  // of one half of one tile
-            mbar_arrive_expect_tx(&s.q_full, bytes * (d.two ? 4u : 2u));
-            for (int x = 0; x <= d.two; ++x) {
-              tma_load_4d(s.q[x], q_map, 0, 0, h, d.tok0 + x * a.tile_tok, &s.q_full);
-              tma_load_4d(s.q[x] + kHalfBytes, q_map, 64, 0, h, d.tok0 + x * a.tile_tok, &s.q_full);
+            mbar_arrive_expect_tx(&s.q_full, bytes * (two ? 4u : 2u));
+            for (int x = 0; x <= two; ++x) {
+              tma_load_4d(s.q[x], q_map, 0, 0, h, tok0 + x * a.tile_tok, &s.q_full);
+              tma_load_4d(s.q[x] + kHalfBytes, q_map, 64, 0, h, tok0 + x * a.tile_tok, &s.q_full);
             }
             ++n_q;
+            post();  // behind the loads that the first scores wait for
           }
         }
         ok = ok && load(row + kPage);
       }
     }
+    ++n_part;
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   }
   if (n_part == 0 && lane == 0) {  // nothing for this CTA
