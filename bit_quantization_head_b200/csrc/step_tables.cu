@@ -14,7 +14,9 @@
 // CTA writes is read.  Where outputs replace their inputs (lengths, ring state) the last
 // CTA to finish reading writes them (one counter); otherwise the first CTA does, at once.
 // Up to 128 sequences a CTA has 128 threads (a step's barriers and launch cost less), for
-// more 1024 with two sequences each.
+// more 1024 with two sequences each.  Measured: 4.6 us for a step of 16 sequences (6.2
+// with 1024 threads), 10 us for 2048 sequences with 600000 rows (20 with two barriers per
+// scan and one sequence per thread).
 #include <cuda_runtime.h>
 
 #include <algorithm>
