@@ -6,15 +6,18 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import hashlib
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvtc.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -51,10 +54,38 @@ def _compile(src, verbose):
     return obj, p.stdout + p.stderr
 
 
+def _build_marshal():
+    """The binding's compiled half (csrc/marshal.cpp): a CPython module against torch."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    src = os.path.join(CSRC, "marshal.cpp")
+    h = hashlib.sha256()
+    for path in (src, os.path.join(ROOT, "include", "kvtc.h"), os.path.join(torch_dir, "version.py")):
+        h.update(open(path, "rb").read())
+    h.update(sys.version.encode())
+    out = os.path.join(BUILD, f"_marshal.{h.hexdigest()[:16]}.so")
+    if not os.path.exists(out):
+        inc = os.path.join(torch_dir, "include")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I" + os.path.join(ROOT, "include"),
+               "-I" + sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
+               os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", "/usr/local/cuda/include", src, "-o",
+               out + ".tmp", "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+        p = subprocess.run(cmd, capture_output=True, text=True)
+        if p.returncode != 0:
+            raise RuntimeError(f"compile failed: marshal.cpp\n{p.stdout}\n{p.stderr}")
+        os.replace(out + ".tmp", out)
+    with open(out, "rb") as f:
+        data = f.read()
+    with open(MARSHAL + ".tmp", "wb") as f:
+        f.write(data)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+
+
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=max(2, os.cpu_count() or 2)) as ex:
+        marshal = ex.submit(_build_marshal)
         results = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        marshal.result()
     objs = [r[0] for r in results]
     if verbose:
         for (o, log), s in zip(results, SOURCES):

@@ -65,6 +65,7 @@ class RawCacheDesc(C.Structure):
 
 
 _lib = None
+_marshal = None  # the compiled half of the calls around the cache, bound to the library
 _P = C.c_void_p
 
 
@@ -158,13 +159,9 @@ def _stream(stream):
     return _P(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
 
 
-def _stream_on(device, stream):
-    """The same for a call whose device is known (a few us less than the public lookup)."""
-    if stream is not None:
-        return _stream(stream)
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return _stream(None) if raw is None else raw(device)
+def _stream_or_none(stream):
+    """A stream's handle for the compiled half (None: the current one)."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _dtype_code(t):
@@ -357,88 +354,37 @@ def kvtc_decode_attention_rope(plan, cache, layer, q, seq_lens, max_seq_len, out
 
 
 # ---------------------------------------------------------------- serving step
-# Checks of these calls read each tensor's properties once and compare objects, not texts:
-# a call of the smallest sizes is bound by the host (about 36 us before, 8 us after for the
-# twelve tensors of kvtc_step_tables).
-_raw_dtypes = {}
+# The tensors of these calls are checked and passed on by csrc/marshal.cpp: the smallest
+# calls are bound by the host (a decode step's tables took 36 us through ctypes, 10 us with
+# the checks in Python).
+def _native():
+    global _marshal
+    if _marshal is None:
+        import importlib.machinery
+        import importlib.util
 
-
-def _raw_dtype(dtype):
-    """Library code of a torch dtype that the calls around the cache take."""
-    if not _raw_dtypes:
-        import torch
-        _raw_dtypes.update({torch.float32: KVTC_F32, torch.bfloat16: KVTC_BF16, torch.float16: KVTC_F16})
-    code = _raw_dtypes.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return code
-
-
-def _device(t, name):
-    """Index of the device of a tensor, which must be the current one."""
-    import torch
-    d = t.get_device()
-    if d < 0 or d != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    return d
-
-
-def _buf(t, dtype, name, device, shape=None):
-    """Device pointer of a contiguous tensor on one device, of one dtype (and shape)."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the current CUDA device")
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _rows(t, dtype, name, device, n_tok):
-    """(pointer, token stride, heads) of rows [n_tok][heads][128] whose heads and elements
-    are dense (a slice of a fused projection passes as it is)."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the current CUDA device")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != HEAD_DIM or shape[0] != n_tok:
-        raise ValueError(f"{name} must have shape [n_tok][heads][{HEAD_DIM}], got {tuple(shape)}")
-    heads = shape[1]
-    stride = t.stride()
-    if stride[2] != 1 or (heads > 1 and stride[1] != HEAD_DIM):
-        raise ValueError(f"{name}: heads and elements must be dense")
-    return t.data_ptr(), (stride[0] if n_tok > 1 else max(heads * HEAD_DIM, 1)), heads
+        import torch  # noqa: F401  (the module's libraries)
+        L = lib()
+        path = os.path.join(_HERE, "_marshal.so")
+        if not os.path.exists(path):
+            raise OSError(f"{path} not built: run `python -m bit_quantization_head_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+        spec = importlib.util.spec_from_file_location("_marshal", path, loader=loader)
+        m = importlib.util.module_from_spec(spec)
+        loader.exec_module(m)
+        m.bind(*(C.cast(f, _P).value for f in (L.kvtc_step_tables, L.kvtc_rope, L.kvtc_raw_append,
+                                               L.kvtc_raw_decode_attention, L.kvtc_raw_cross_attention)))
+        _marshal = m
+    return _marshal
 
 
 def kvtc_step_tables(cached_lens, new_lens, page_ring, ring_state, block_table, seq_lens, cu_seqlens, slot_map,
                      positions, ring_state_out, workspace, status=None, stream=None):
     """Tables of one serving step from the request lengths (all device tensors; int32, the
     slot map int64).  ring_state_out may be ring_state and seq_lens may be cached_lens."""
-    import torch
-    i32, dev = torch.int32, _device(cached_lens, "cached_lens")
-    n_seq, rows, capacity = cached_lens.numel(), slot_map.numel(), page_ring.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have shape [n_seq][max_pages]")
-    max_pages = block_table.shape[1]
-    if workspace.nbytes < 16:
-        raise ValueError("workspace must hold 16 bytes")
-    p = []
-    for t, name, n in ((cached_lens, "cached_lens", n_seq), (new_lens, "new_lens", n_seq),
-                       (page_ring, "page_ring", capacity), (ring_state, "ring_state", 2),
-                       (block_table, "block_table", n_seq * max_pages), (seq_lens, "seq_lens", n_seq),
-                       (cu_seqlens, "cu_seqlens", n_seq + 1), (positions, "positions", rows),
-                       (ring_state_out, "ring_state_out", 2)):
-        if t.get_device() != dev or t.dtype is not i32 or not t.is_contiguous() or t.numel() != n:
-            _buf(t, i32, name, dev)
-            raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
-        p.append(t.data_ptr())
-    st = lib().kvtc_step_tables(
-        p[0], p[1], n_seq, p[2], capacity, p[3], p[4], max_pages, p[5], p[6], _buf(slot_map, torch.int64, "slot_map", dev),
-        p[7], rows, p[8], _buf(workspace, None, "workspace", dev),
-        None if status is None else _buf(status, i32, "status", dev), _stream_on(dev, stream))
+    st = (_marshal or _native()).step_tables(cached_lens, new_lens, page_ring, ring_state, block_table, seq_lens,
+                                             cu_seqlens, slot_map, positions, ring_state_out, workspace, status,
+                                             _stream_or_none(stream))
     if st:
         _check(st)
 
@@ -452,35 +398,18 @@ def rope_desc(sections, interleaved=False, base=0.0):
     return RopeDesc(len(sections), (C.c_int * 4)(*sections), 1 if interleaved else 0, float(base))
 
 
-_NO_ROWS = (None, 0, 0)
-
-
 def kvtc_rope(rope, q, k, positions, q_out, k_out, inverse=False, stream=None):
     """Rotates q and/or k rows [n_tok][heads][128] to positions int32 [n_axes][n_tok]
     (or [n_tok] for one axis); inverse: the transpose.  q or k may be None."""
-    ref = q if q is not None else k
-    if ref is None:
-        raise ValueError("q or k must be given")
-    dtype, n_tok = ref.dtype, ref.shape[0]
-    code, dev = _raw_dtype(dtype), _device(ref, "q" if q is not None else "k")
-    qp = _rows(q, dtype, "q", dev, n_tok) if q is not None else _NO_ROWS
-    kp = _rows(k, dtype, "k", dev, n_tok) if k is not None else _NO_ROWS
-    st = lib().kvtc_rope(
-        C.byref(rope), *qp, *kp, code, _positions_ptr(rope, positions, n_tok, dev), n_tok, 1 if inverse else 0,
-        None if q is None else _buf(q_out, dtype, "q_out", dev, q.shape),
-        None if k is None else _buf(k_out, dtype, "k_out", dev, k.shape), _stream_on(dev, stream))
+    st = (_marshal or _native()).rope(C.addressof(rope), q, k, positions, q_out, k_out, inverse, _stream_or_none(stream))
     if st:
         _check(st)
 
 
-def _positions_ptr(rope, positions, n_tok, device):
-    import torch
-    if positions.numel() != rope.n_axes * n_tok or positions.shape[-1] != n_tok:
-        raise ValueError(f"positions must have shape [{rope.n_axes}][{n_tok}]")
-    return _buf(positions, torch.int32, "positions", device)
-
-
 # ---------------------------------------------------------------- uncompressed pages
+_RAW_DTYPES = {"torch.bfloat16": KVTC_BF16, "torch.float16": KVTC_F16}
+
+
 def kvtc_raw_cache_bytes(n_layers, n_pages, n_kv_heads):
     return int(lib().kvtc_raw_cache_bytes(n_layers, n_pages, n_kv_heads))
 
@@ -494,7 +423,7 @@ class RawCache:
     def __init__(self, n_layers, n_kv_heads, n_pages, block_table, dtype=None, device="cuda", pool=None):
         import torch
         dtype = torch.bfloat16 if dtype is None else dtype
-        if dtype not in (torch.bfloat16, torch.float16):
+        if str(dtype) not in _RAW_DTYPES:
             raise TypeError(f"unsupported dtype {dtype}")
         shape = (int(n_layers), int(n_pages), int(n_kv_heads), 2, PAGE_TOKENS, HEAD_DIM)
         if pool is None:
@@ -506,28 +435,18 @@ class RawCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self.dtype = dtype
         self.n_kv_heads = shape[2]
-        self.n_seq = self.block_table.shape[0]
-        self.desc = RawCacheDesc(pool.data_ptr(), shape[0], shape[1], shape[2], _raw_dtype(dtype),
-                                 self.block_table.data_ptr(), self.n_seq, self.block_table.shape[1],
+        self.desc = RawCacheDesc(pool.data_ptr(), shape[0], shape[1], shape[2], _RAW_DTYPES[str(dtype)],
+                                 self.block_table.data_ptr(), self.block_table.shape[0], self.block_table.shape[1],
                                  self.status.data_ptr())
+        self._address = C.addressof(self.desc)
 
 
 def kvtc_raw_append(cache, layer, k, v, slot_map, rope=None, positions=None, q=None, q_out=None, stream=None):
     """Writes k, v rows [n_tok][n_kv_heads][128] into their slots (int64 [n_tok]) of one
     layer's pages; with rope, k is rotated on the way, and q into q_out."""
-    import torch
-    n_tok, dtype, dev = k.shape[0], cache.dtype, _device(cache.pool, "the cache")
-    kp, vp = _rows(k, dtype, "k", dev, n_tok), _rows(v, dtype, "v", dev, n_tok)
-    if kp[2] != cache.n_kv_heads or vp[2] != cache.n_kv_heads:
-        raise ValueError(f"k and v must have {cache.n_kv_heads} heads")
-    if rope is not None and positions is None:
-        raise ValueError("rope needs positions")
-    qp = _rows(q, dtype, "q", dev, n_tok) if q is not None else _NO_ROWS
-    st = lib().kvtc_raw_append(
-        C.byref(cache.desc), layer, kp[0], kp[1], vp[0], vp[1], _buf(slot_map, torch.int64, "slot_map", dev, (n_tok,)),
-        n_tok, None if rope is None else C.byref(rope),
-        None if rope is None else _positions_ptr(rope, positions, n_tok, dev), *qp,
-        None if q is None else _buf(q_out, dtype, "q_out", dev, q.shape), _stream_on(dev, stream))
+    st = (_marshal or _native()).raw_append(cache._address, cache.pool, layer, k, v, slot_map,
+                                            None if rope is None else C.addressof(rope), positions, q, q_out,
+                                            _stream_or_none(stream))
     if st:
         _check(st)
 
@@ -540,23 +459,11 @@ def kvtc_raw_cross_workspace_bytes(n_seq, n_tok, n_q_heads, n_kv_heads, max_seq_
     return int(lib().kvtc_raw_cross_workspace_bytes(n_seq, n_tok, n_q_heads, n_kv_heads, max_seq_len))
 
 
-def _head_rows(cache, t, name, rows, device):
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != rows or shape[2] != HEAD_DIM:
-        raise ValueError(f"{name} must have shape [{rows}][n_q_heads][{HEAD_DIM}], got {tuple(shape)}")
-    return _buf(t, cache.dtype, name, device)
-
-
 def kvtc_raw_decode_attention(cache, layer, q, seq_lens, max_seq_len, out, workspace, scale=0.0, stream=None):
     """One new token per sequence over one layer's uncompressed pages; q, out
     [n_seq][n_q_heads][128] of the cache's dtype."""
-    import torch
-    n_seq, dev = cache.n_seq, _device(cache.pool, "the cache")
-    st = lib().kvtc_raw_decode_attention(
-        C.byref(cache.desc), layer, _head_rows(cache, q, "q", n_seq, dev), q.shape[1],
-        _buf(seq_lens, torch.int32, "seq_lens", dev, (n_seq,)), max_seq_len, scale,
-        _buf(out, cache.dtype, "out", dev, q.shape), _buf(workspace, None, "workspace", dev), workspace.nbytes,
-        _stream_on(dev, stream))
+    st = (_marshal or _native()).raw_decode(cache._address, cache.pool, layer, q, seq_lens, max_seq_len, out, workspace,
+                                            scale, _stream_or_none(stream))
     if st:
         _check(st)
 
@@ -564,13 +471,7 @@ def kvtc_raw_decode_attention(cache, layer, q, seq_lens, max_seq_len, out, works
 def kvtc_raw_cross_attention(cache, layer, q, cu_q, seq_lens, max_seq_len, out, workspace, scale=0.0, stream=None):
     """Rows cu_q[s]..cu_q[s+1]-1 of q [n_tok][n_q_heads][128] attend to the first seq_lens[s]
     tokens of sequence s's uncompressed pages (no causal mask)."""
-    import torch
-    n_seq, n_tok, dev = cache.n_seq, q.shape[0], _device(cache.pool, "the cache")
-    st = lib().kvtc_raw_cross_attention(
-        C.byref(cache.desc), layer, _head_rows(cache, q, "q", n_tok, dev), q.shape[1],
-        _buf(cu_q, torch.int32, "cu_q", dev, (n_seq + 1,)), n_tok,
-        _buf(seq_lens, torch.int32, "seq_lens", dev, (n_seq,)), max_seq_len, scale,
-        _buf(out, cache.dtype, "out", dev, q.shape), _buf(workspace, None, "workspace", dev), workspace.nbytes,
-        _stream_on(dev, stream))
+    st = (_marshal or _native()).raw_cross(cache._address, cache.pool, layer, q, cu_q, seq_lens, max_seq_len, out,
+                                           workspace, scale, _stream_or_none(stream))
     if st:
         _check(st)

@@ -268,3 +268,58 @@ def test_rope_and_its_transpose_give_the_rows_back():
     kvtc.kvtc_rope(d, out, None, pos, out, None, inverse=True)
     # both rotations' errors, the second's on rows as large as the first's
     assert ((out.double() - q.double()).abs() <= 2.5 * ref.rope_bound(q, torch.float32)).all()
+
+
+# ------------------------------------------------------------------ the binding's refusals
+def test_the_binding_refuses_types_shapes_and_strides():
+    cache, _ = states([100, 50], 2, torch.bfloat16, 90)
+    q, lens = rand_q(2, 4, torch.bfloat16, 91), i32([100, 50])
+    out, ws = torch.empty_like(q), decode_ws(2, 4, 2, 100)
+    good = dict(q=q, lens=lens, out=out, ws=ws)
+    for change, error in ((dict(q=q.half()), TypeError), (dict(lens=lens.long()), TypeError), (dict(out=out.float()), TypeError),
+                          (dict(q=q[:1]), ValueError), (dict(q=q[..., :64]), ValueError), (dict(lens=i32([1, 2, 3])), ValueError),
+                          (dict(out=out[:, :2]), ValueError), (dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), ValueError),
+                          (dict(lens=lens.cpu()), ValueError), (dict(ws=ws.cpu()), ValueError), (dict(ws=ws[:100]), kvtc.KvtcError)):
+        a = dict(good, **change)
+        with pytest.raises(error):
+            kvtc.kvtc_raw_decode_attention(cache, 1, a["q"], a["lens"], 100, a["out"], a["ws"])
+    with pytest.raises(ValueError):                    # beyond the library's int
+        kvtc.kvtc_raw_decode_attention(cache, 1, q, lens, 1 << 40, out, ws)
+    with pytest.raises(TypeError):
+        kvtc.kvtc_raw_decode_attention(cache, "1", q, lens, 100, out, ws)
+    with pytest.raises(kvtc.KvtcError):
+        kvtc.kvtc_raw_decode_attention(cache, 2, q, lens, 100, out, ws)
+    with pytest.raises(kvtc.KvtcError):
+        kvtc.kvtc_raw_decode_attention(cache, 1, q, lens, 100, q, ws)
+    k = rand_q(3, 2, torch.bfloat16, 92)
+    slots = torch.arange(3, device="cuda")
+    for bad in (dict(k=rand_q(3, 3, torch.bfloat16, 1)), dict(v=k[:2]), dict(slots=slots[:2]), dict(slots=slots.int()),
+                dict(k=k.half()), dict(k=k.transpose(0, 1).contiguous().transpose(0, 1))):
+        a = dict(dict(k=k, v=k, slots=slots), **bad)
+        with pytest.raises((TypeError, ValueError)):
+            kvtc.kvtc_raw_append(cache, 1, a["k"], a["v"], a["slots"])
+    with pytest.raises(ValueError):                    # rope without positions
+        kvtc.kvtc_raw_append(cache, 1, k, k, slots, rope=kvtc.rope_desc([64]))
+    with pytest.raises(ValueError):                    # positions of another shape
+        kvtc.kvtc_rope(kvtc.rope_desc([32, 32]), q, None, i32([1, 2]), out, None)
+    with pytest.raises(kvtc.KvtcError):                # q without a rotation
+        kvtc.kvtc_raw_append(cache, 1, k, k, slots, q=k, q_out=torch.empty_like(k))
+    torch.cuda.synchronize()
+    assert cache.status.item() == 0
+
+
+def test_a_stream_handle_an_int_and_the_current_stream():
+    cache, kv = states([300], 2, torch.bfloat16, 93)
+    q, lens, ws = rand_q(1, 4, torch.bfloat16, 94), i32([300]), decode_ws(1, 4, 2, 300)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side, side.cuda_stream):
+        out = torch.full_like(q, float("nan"))
+        torch.cuda.synchronize()
+        if stream is None:
+            with torch.cuda.stream(side):
+                kvtc.kvtc_raw_decode_attention(cache, 1, q, lens, 300, out, ws)
+        else:
+            kvtc.kvtc_raw_decode_attention(cache, 1, q, lens, 300, out, ws, stream=stream)
+        side.synchronize()
+        ref.assert_close(out, *ref.attention(q, *kv[0]))
