@@ -18,10 +18,10 @@ constexpr long long kKindElems = static_cast<long long>(kPage) * kD;  // K or V 
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Whether two buffers of the same size share memory.
-inline bool overlap(const void* a, const void* b, uint64_t bytes) {
+// Whether two buffers share memory (null or empty ones do not).
+inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + bytes && y < x + bytes;
+  return a && b && na && nb && x < y + nb && y < x + na;
 }
 
 // The sizes and pointers every call on the uncompressed pages needs.
@@ -54,6 +54,21 @@ inline kvtc_status check_attention(const kvtc_raw_cache* c, int layer, int n_q_h
   if (max_seq_len < 0 || max_seq_len > static_cast<long long>(c->max_pages) * kPage)
     return fail(KVTC_EINVAL, "max_seq_len exceeds the block table");
   if (!std::isfinite(scale) || scale < 0.0f) return fail(KVTC_EINVAL, "softmax_scale must be finite and >= 0");
+  return KVTC_OK;
+}
+
+inline uint64_t pool_bytes(const kvtc_raw_cache* c) {
+  return static_cast<uint64_t>(c->n_layers) * c->n_pages * static_cast<uint64_t>(c->n_kv_heads) * 2 * kKindElems * 2;
+}
+
+// What an attention call writes shares memory with nothing else that it touches.
+inline kvtc_status check_overlap(const kvtc_raw_cache* c, const void* q, const void* out, uint64_t rows, const void* ws,
+                                 uint64_t ws_bytes) {
+  if (overlap(q, rows, out, rows)) return fail(KVTC_EINVAL, "out overlaps q");
+  if (overlap(out, rows, c->pool, pool_bytes(c)) || overlap(out, rows, ws, ws_bytes))
+    return fail(KVTC_EINVAL, "out overlaps the pool or the workspace");
+  if (overlap(ws, ws_bytes, c->pool, pool_bytes(c)) || overlap(ws, ws_bytes, q, rows))
+    return fail(KVTC_EINVAL, "the workspace overlaps the pool or q");
   return KVTC_OK;
 }
 

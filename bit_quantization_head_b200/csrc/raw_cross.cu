@@ -97,7 +97,7 @@ struct __align__(1024) Smem {
   uint64_t kv_full[kStages], kv_empty[kStages], q_full, q_empty, part_full[2], part_empty[2];
   uint64_t s_full[2], p_full[2][2], o_full[2], twin_full, twin_empty, drain;
   int dead;
-  int arrived[2][2];       // [tile][part & 1]
+  int arrived[2][2];       // [tile][a unit from an earlier CTA, one that goes on in the next]
   float2 twin_ml[kRows];   // the second tile's m and l of a twin part
   uint32_t tmem;
 };
@@ -771,7 +771,7 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
       const bool whole = d.first && d.last;
       const int shares = d.c1 - d.c0 + 1;
       int* ticket = a.tickets + 2 * d.c0 + x;
-      if (!whole && row == 0) s.arrived[x][n & 1] = ld_acquire_gpu(ticket);
+      if (!whole && row == 0) s.arrived[x][d.first] = ld_acquire_gpu(ticket);
       if (some) {
         if (!wait(&s.o_full[x], n_o++ & 1)) return;
         tc_fence_after();
@@ -840,7 +840,7 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
         if (!tile_sync()) return;
         const int rows = min(a.tile_tok, d.tok1 - d.tok0 - x * a.tile_tok) * a.G;
         const bool few = rows <= 32;
-        bool join = !few && s.arrived[x][n & 1] == shares - 1;
+        bool join = !few && s.arrived[x][d.first] == shares - 1;
         if (!join) {
           float* mine = part_of(a, blockIdx.x, d.first, x);
           if (live) reinterpret_cast<float2*>(mine)[row] = make_float2(m, l);
@@ -856,9 +856,9 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
           }
           __threadfence();
           if (!tile_sync()) return;
-          if (row == 0) s.arrived[x][n & 1] = atomicAdd(ticket, 1);
+          if (row == 0) s.arrived[x][d.first] = atomicAdd(ticket, 1);
           if (!tile_sync()) return;
-          join = s.arrived[x][n & 1] == shares - 1;
+          join = s.arrived[x][d.first] == shares - 1;
         }
         if (join && few) {
           __threadfence();
@@ -1041,8 +1041,9 @@ extern "C" kvtc_status kvtc_raw_cross_attention(const kvtc_raw_cache* cache, int
     return fail(KVTC_EINVAL, "q, out and workspace must be 16-byte aligned");
   if (workspace_bytes < kvtc_raw_cross_workspace_bytes(cache->n_seq, n_tok, n_q_heads, cache->n_kv_heads, max_seq_len))
     return fail(KVTC_ECAPACITY, "cross attention workspace too small");
-  if (raw::overlap(q, out, static_cast<uint64_t>(n_tok) * n_q_heads * kD * 2))
-    return fail(KVTC_EINVAL, "out overlaps q");
+  st = raw::check_overlap(cache, q, out, static_cast<uint64_t>(n_tok) * n_q_heads * kD * 2, workspace,
+                          kvtc_raw_cross_workspace_bytes(cache->n_seq, n_tok, n_q_heads, cache->n_kv_heads, max_seq_len));
+  if (st != KVTC_OK) return st;
   int sms = 0;
   st = raw::sm_count(&sms);
   if (st != KVTC_OK) return st;

@@ -671,8 +671,9 @@ extern "C" kvtc_status kvtc_raw_decode_attention(const kvtc_raw_cache* cache, in
     return fail(KVTC_EINVAL, "q, out and workspace must be 16-byte aligned");
   if (workspace_bytes < kvtc_raw_decode_workspace_bytes(cache->n_seq, n_q_heads, cache->n_kv_heads, max_seq_len))
     return fail(KVTC_ECAPACITY, "decode workspace too small");
-  if (raw::overlap(q, out, static_cast<uint64_t>(cache->n_seq) * n_q_heads * kD * 2))
-    return fail(KVTC_EINVAL, "out overlaps q");
+  st = raw::check_overlap(cache, q, out, static_cast<uint64_t>(cache->n_seq) * n_q_heads * kD * 2, workspace,
+                          kvtc_raw_decode_workspace_bytes(cache->n_seq, n_q_heads, cache->n_kv_heads, max_seq_len));
+  if (st != KVTC_OK) return st;
   int sms = 0;
   st = raw::sm_count(&sms);
   if (st != KVTC_OK) return st;

@@ -196,7 +196,7 @@ kvtc_status check_rows(const void* x, int64_t stride, int heads, size_t es, cons
 
 // No output may share memory with an input or the other output, but for rows rotated in
 // place (the same contiguous rows).
-kvtc_status check_overlap(const RopeArgs& a, size_t es) {
+kvtc_status check_rope_overlap(const RopeArgs& a, size_t es, const kvtc_raw_cache* cache) {
   const void* out[2] = {a.q_out, a.k_out};
   uint64_t span[3], dense[3];
   for (int i = 0; i < 3; ++i) {
@@ -204,17 +204,18 @@ kvtc_status check_overlap(const RopeArgs& a, size_t es) {
     span[i] = static_cast<uint64_t>(a.n_tok - 1) * static_cast<uint64_t>(a.stride[i]) * es +
               static_cast<uint64_t>(a.heads[i]) * kD * es;
   }
-  auto meet = [](const void* p, uint64_t np, const void* q, uint64_t nq) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
-    return p && q && x < y + nq && y < x + np;
-  };
   for (int o = 0; o < 2; ++o) {
     for (int i = 0; i < 3; ++i) {
       const bool same = o == i && out[o] == a.x[i] && a.stride[i] == static_cast<long long>(a.heads[i]) * kD;
-      if (!same && meet(out[o], dense[o], a.x[i], span[i])) return fail(KVTC_EINVAL, "an output overlaps an input");
+      if (!same && raw::overlap(out[o], dense[o], a.x[i], span[i])) return fail(KVTC_EINVAL, "an output overlaps an input");
     }
   }
-  if (meet(out[0], dense[0], out[1], dense[1])) return fail(KVTC_EINVAL, "the outputs overlap");
+  if (raw::overlap(out[0], dense[0], out[1], dense[1])) return fail(KVTC_EINVAL, "the outputs overlap");
+  if (cache) {
+    bool pool = raw::overlap(out[0], dense[0], cache->pool, raw::pool_bytes(cache));
+    for (int i = 0; i < 3; ++i) pool |= raw::overlap(a.x[i], span[i], cache->pool, raw::pool_bytes(cache));
+    if (pool) return fail(KVTC_EINVAL, "rows overlap the pool");
+  }
   return KVTC_OK;
 }
 
@@ -276,7 +277,7 @@ extern "C" kvtc_status kvtc_rope(const kvtc_rope_desc* rope, const void* q, int6
   a.k_out = k_out;
   a.positions = positions;
   a.n_tok = n_tok;
-  st = check_overlap(a, es);
+  st = check_rope_overlap(a, es, nullptr);
   if (st != KVTC_OK) return st;
   return launch_rope(a, dtype, stream);
 }
@@ -323,7 +324,7 @@ extern "C" kvtc_status kvtc_raw_append(const kvtc_raw_cache* cache, int layer, c
   a.positions = positions;
   a.n_tok = n_tok;
   a.status = cache->status;
-  st = check_overlap(a, 2);
+  st = check_rope_overlap(a, 2, cache);
   if (st != KVTC_OK) return st;
   return launch_rope(a, cache->dtype, stream);
 }

@@ -302,12 +302,6 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const __grid_cons
   }
 }
 
-// Whether two buffers share memory (null or empty ones do not).
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && na && nb && x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace kvtc
 
@@ -339,7 +333,7 @@ extern "C" kvtc_status kvtc_step_tables(const int32_t* cached_lens, const int32_
     if (reinterpret_cast<uintptr_t>(buf[i].p) & (i == 7 ? 7 : 3)) return fail(KVTC_EINVAL, "misaligned device pointer");
     for (int j = i + 1; j < count; ++j) {
       const bool in_place = ((i == 0 && j == 5) || (i == 3 && j == 9)) && buf[i].p == buf[j].p;
-      if (!in_place && overlap(buf[i].p, buf[i].bytes, buf[j].p, buf[j].bytes))
+      if (!in_place && raw::overlap(buf[i].p, buf[i].bytes, buf[j].p, buf[j].bytes))
         return fail(KVTC_EINVAL, "buffers overlap");
     }
   }

@@ -42,3 +42,26 @@ def test_what_is_no_tensor_is_refused():
         kvtc.kvtc_rope(kvtc.rope_desc([64]), None, None, i, None, None)
     with pytest.raises(TypeError, match="unsupported dtype"):
         kvtc.kvtc_rope(kvtc.rope_desc([64]), torch.zeros((2, 3, 128), dtype=torch.float64), None, i, i, None)
+
+
+# ------------------------------------------------------------------ buffers that overlap
+A = 1 << 30          # stands for aligned device addresses far apart; never dereferenced
+
+
+def raw_cache():
+    return kvtc.RawCacheDesc(8 * A, 2, 64, 2, kvtc.KVTC_BF16, 9 * A, 3, 8, None)
+
+
+def test_attention_refuses_outputs_and_workspaces_in_the_pool():
+    L, c = kvtc.lib(), kvtc.C.byref(raw_cache())
+    pool = 8 * A + 4096
+    for q, out, ws in ((A, pool, 3 * A), (A, 2 * A, pool), (A, 3 * A + 4096, 3 * A), (3 * A + 256, 2 * A, 3 * A)):
+        assert L.kvtc_raw_decode_attention(c, 0, q, 8, 4 * A, 1000, 0.0, out, ws, 1 << 29, None) == 1
+        assert L.kvtc_raw_cross_attention(c, 0, q, 8, 5 * A, 100, 4 * A, 1000, 0.0, out, ws, 1 << 29, None) == 1
+
+
+def test_append_refuses_rows_in_the_pool():
+    L, c, pool = kvtc.lib(), kvtc.C.byref(raw_cache()), 8 * A + 8192
+    d = kvtc.C.byref(kvtc.rope_desc([64]))
+    for k, v, q, out in ((pool, A, 2 * A, 3 * A), (A, pool, 2 * A, 3 * A), (A, 4 * A, pool, 3 * A), (A, 4 * A, 2 * A, pool)):
+        assert L.kvtc_raw_append(c, 0, k, 256, v, 256, 5 * A, 8, d, 6 * A, q, 512, 4, out, None) == 1
