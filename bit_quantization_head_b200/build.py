@@ -1,4 +1,5 @@
-"""Builds libkvtc.so in-tree for sm_100a (nvcc cross-compiles without a GPU).
+"""Builds libkvtc.so in-tree for sm_100a (nvcc cross-compiles without a GPU) and _marshal.so,
+the binding's compiled half.
 
 python -m bit_quantization_head_b200.build [--verbose]
 """

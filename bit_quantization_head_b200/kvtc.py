@@ -1,7 +1,7 @@
-"""ctypes binding of libkvtc (include/kvtc.h): the same entry points, argument
-marshalling only.  Every step of the encode/decode path runs in the library's CUDA
-kernels; calibration runs in its C++ host code.  There is no Python or CPU fallback:
-if libkvtc.so is missing, ``lib()`` raises.
+"""Binding of libkvtc (include/kvtc.h): the same entry points, argument marshalling only
+(ctypes; the calls around the cache check their tensors in csrc/marshal.cpp).  Every step
+of the encode/decode path runs in the library's CUDA kernels; calibration runs in its C++
+host code.  There is no Python or CPU fallback: if libkvtc.so is missing, ``lib()`` raises.
 
 Host arrays are numpy; device buffers are torch CUDA tensors (torch provides device
 memory and streams only).
