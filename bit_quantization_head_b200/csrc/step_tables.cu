@@ -8,15 +8,15 @@
 //
 // Bound: latency for a decode step (a launch, two dependent loads, two scans), the 12
 // bytes per row for large steps.  One launch without a wait between CTAs: every CTA scans
-// all sequences for itself (8 bytes each, from L2) and fills its own range of rows; a row
-// finds its sequence by bisection in the chunk's prefix sums in shared memory and takes
-// its page id straight from the ring or the old table entries, so nothing that another
+// all sequences for itself (8 bytes each, from L2) and fills its own range of rows; the rows
+// find their sequences by a running maximum over the marks of the first rows, and take
+// their page ids straight from the ring or the old table entries, so nothing that another
 // CTA writes is read.  Where outputs replace their inputs (lengths, ring state) the last
 // CTA to finish reading writes them (one counter); otherwise the first CTA does, at once.
 // Up to 128 sequences a CTA has 128 threads (a step's barriers and launch cost less), for
-// more 1024 with two sequences each.  Measured: 4.6 us for a step of 16 sequences (6.2
-// with 1024 threads), 10 us for 2048 sequences with 600000 rows (20 with two barriers per
-// scan and one sequence per thread).
+// more 1024 with two sequences each.  Measured: 4.3 us for a step of 16 sequences (6.2 with
+// 1024 threads and 64-bit scans), 7.6 us for 2048 sequences with 600000 rows (20 with two
+// barriers per scan, a bisection per row and one sequence per thread).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -50,18 +50,20 @@ struct TablesArgs {
   int32_t* status;
 };
 
-template <int kThreads, int kPer>
+template <typename T, int kThreads, int kPer>
 struct Smem {
   static constexpr int kWarps = kThreads / 32, kChunk = kThreads * kPer;
-  long long rows_sum[kWarps], released_sum[kWarps];
+  T rows_sum[kWarps], released_sum[kWarps];
   int need_sum[kWarps];
   int taken;                  // pages taken from the ring's head
   int last;
   int first_row[kChunk + 1];  // rows of the chunk's sequences, clipped to n_rows
   int cached[kChunk];
-  int page0[kChunk];          // ring offset (from the head) of the sequence's first new page
   int need[kChunk];           // new pages (-1: the sequence keeps its length; -2: finished)
-  int release0[kChunk];       // ring offset (from the tail) of its first released page
+  int offset[kChunk];         // of its first new page from the ring's head, or of the first
+                              // released one from its tail
+  alignas(8) uint16_t owner[kThreads * kRowsPerThread];  // sequence (of the chunk) of each row
+  int owner_max[kWarps];
 };
 
 // Exclusive sum over the block's warps of one value per thread (incl: the warp's inclusive
@@ -91,9 +93,11 @@ struct Carry {
 };
 
 // Decides the chunk of sequences from base on (kPer consecutive ones per thread) into
-// shared memory; ends with a barrier.
-template <int kThreads, int kPer>
-__device__ uint32_t decide(const TablesArgs& a, Smem<kThreads, kPer>& s, int base, int count, Carry& run,
+// shared memory; ends with a barrier.  T: the type of a chunk's sums of rows and of released
+// pages; int where they fit (a length beyond n_rows then counts as n_rows + 1, which leaves
+// no row to it or to a later sequence either), as 64-bit scans take twice the shuffles.
+template <typename T, int kThreads, int kPer>
+__device__ uint32_t decide(const TablesArgs& a, Smem<T, kThreads, kPer>& s, int base, int count, Carry& run,
                            int (&new_len)[kPer]) {
   constexpr int kWarps = kThreads / 32;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -101,7 +105,8 @@ __device__ uint32_t decide(const TablesArgs& a, Smem<kThreads, kPer>& s, int bas
   int c[kPer], n[kPer], held[kPer];
   bool bad[kPer];
   uint32_t flags = 0;
-  long long row = 0, rel = 0;
+  const int most_rows = sizeof(T) == 4 ? a.n_rows + 1 : INT32_MAX;
+  T row_sum = 0, rel_sum = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int q = base + t * kPer + k;
@@ -113,15 +118,15 @@ __device__ uint32_t decide(const TablesArgs& a, Smem<kThreads, kPer>& s, int bas
     bad[k] = c[k] < 0 || c[k] > limit;
     if (bad[k]) flags |= KVTC_STATUS_BAD_POS, c[k] = 0;
     held[k] = (c[k] + kPage - 1) / kPage;
-    row += max(n[k], 0);
-    rel += n[k] < 0 ? held[k] : 0;
+    row_sum += min(max(n[k], 0), most_rows);
+    rel_sum += n[k] < 0 ? held[k] : 0;
   }
-  const long long row_incl = warp_scan(row), rel_incl = warp_scan(rel);
+  const T row_incl = warp_scan(row_sum), rel_incl = warp_scan(rel_sum);
   if (lane == 31) s.rows_sum[warp] = row_incl, s.released_sum[warp] = rel_incl;
   __syncthreads();
-  long long rows_total, rel_total;
-  row = run.rows + block_prefix<kWarps>(s.rows_sum, rows_total) + row_incl - row;
-  rel = run.released + block_prefix<kWarps>(s.released_sum, rel_total) + rel_incl - rel;
+  T rows_total, rel_total;
+  long long row = run.rows + (block_prefix<kWarps>(s.rows_sum, rows_total) + row_incl - row_sum);
+  long long rel = run.released + (block_prefix<kWarps>(s.released_sum, rel_total) + rel_incl - rel_sum);
   run.rows += rows_total;
   run.released += rel_total;
   bool fits[kPer];
@@ -136,7 +141,7 @@ __device__ uint32_t decide(const TablesArgs& a, Smem<kThreads, kPer>& s, int bas
     all += need[k];
     first_row[k] = static_cast<int>(min(row, static_cast<long long>(a.n_rows)));
     release0[k] = static_cast<int>(min(rel, static_cast<long long>(a.capacity)));
-    row += fresh;
+    row += min(fresh, most_rows);
     rel += n[k] < 0 ? held[k] : 0;
   }
   const int need_incl = warp_scan(all);
@@ -155,9 +160,8 @@ __device__ uint32_t decide(const TablesArgs& a, Smem<kThreads, kPer>& s, int bas
     const bool finished = q < a.n_seq && n[k] < 0;
     s.first_row[i] = first_row[k];
     s.cached[i] = c[k];
-    s.page0[i] = grows ? static_cast<int>(min(first, static_cast<long long>(count))) : 0;
     s.need[i] = finished ? -2 : grows ? need[k] : -1;
-    s.release0[i] = release0[k];
+    s.offset[i] = finished ? release0[k] : grows ? static_cast<int>(min(first, static_cast<long long>(count))) : 0;
     new_len[k] = finished ? 0 : grows ? c[k] + n[k] : c[k];
     first += need[k];
   }
@@ -168,10 +172,55 @@ __device__ uint32_t decide(const TablesArgs& a, Smem<kThreads, kPer>& s, int bas
   return flags;
 }
 
-template <int kThreads, int kPer>
+// The sequence of each of the CTA's rows lo .. hi - 1, into shared memory: a sequence marks
+// its first row there, and a running maximum over the rows carries it on (a bisection per row
+// took a third of a large step's time).  Ends with a barrier.
+template <typename T, int kThreads, int kPer>
+__device__ __forceinline__ void find_owners(Smem<T, kThreads, kPer>& s, int n_in, int lo, int hi) {
+  static_assert(kRowsPerThread == 4, "a thread's rows are one 8-byte word");
+  constexpr int kWarps = kThreads / 32;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  uint2* words = reinterpret_cast<uint2*>(s.owner);
+  words[t] = make_uint2(0u, 0u);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = t * kPer + k;
+    if (i < n_in) {
+      const int first = s.first_row[i], end = s.first_row[i + 1];
+      if (first < end && end > lo && first < hi) s.owner[max(first, lo) - lo] = static_cast<uint16_t>(i);
+    }
+  }
+  __syncthreads();
+  const uint2 w = words[t];
+  int m[4] = {static_cast<int>(w.x & 0xFFFFu), static_cast<int>(w.x >> 16), static_cast<int>(w.y & 0xFFFFu),
+              static_cast<int>(w.y >> 16)};
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m[i] = max(m[i], m[i - 1]);
+  auto max_scan = [&](int v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int p = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, p);
+    }
+    return v;
+  };
+  const int incl = max_scan(m[3]);
+  if (lane == 31) s.owner_max[warp] = incl;
+  __syncthreads();
+  const int all = max_scan(lane < kWarps ? s.owner_max[lane] : 0);
+  const int warps = __shfl_sync(0xffffffffu, all, (warp + 31) & 31), lanes = __shfl_up_sync(0xffffffffu, incl, 1);
+  const int before = max(warp ? warps : 0, lane ? lanes : 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = max(m[i], before);
+  words[t] = make_uint2(static_cast<uint32_t>(m[0] | m[1] << 16), static_cast<uint32_t>(m[2] | m[3] << 16));
+  __syncthreads();
+}
+
+template <typename T, int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) step_tables_kernel(const __grid_constant__ TablesArgs a) {
   constexpr int kWarps = kThreads / 32, kChunk = kThreads * kPer, kRowsPerCta = kThreads * kRowsPerThread;
-  __shared__ Smem<kThreads, kPer> s;
+  __shared__ Smem<T, kThreads, kPer> s;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   if (t == 0) s.taken = 0;  // (the scans' barriers come before its first use)
   griddep_wait();
@@ -206,19 +255,10 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const __grid_cons
     const int n_in = min(kChunk, a.n_seq - base);
     // this CTA's rows that fall into the chunk: all of a thread's at once
     const int lo = max(row_lo, s.first_row[0]), hi = min(row_hi, s.first_row[kChunk]);
-    int l[kRowsPerThread], h[kRowsPerThread];  // the last sequence whose first row is <= r
+    int l[kRowsPerThread];  // their sequences
+    if (lo < hi) find_owners(s, n_in, lo, hi);
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) l[i] = 0, h[i] = n_in - 1;
-    if (lo < hi) {
-      for (int span = n_in - 1; span > 0; span >>= 1)
-#pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) {
-          const int r = lo + min(t + i * kThreads, hi - lo - 1), mid = (l[i] + h[i] + 1) >> 1;
-          const bool up = s.first_row[mid] <= r;
-          l[i] = up ? mid : l[i];
-          h[i] = up ? h[i] : max(mid - 1, l[i]);
-        }
-    }
+    for (int i = 0; i < kRowsPerThread; ++i) l[i] = lo < hi ? s.owner[t + i * kThreads] : 0;
     int32_t id[kRowsPerThread];
     int pos[kRowsPerThread];
 #pragma unroll
@@ -230,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const __grid_cons
         const int c = s.cached[l[i]], held = (c + kPage - 1) / kPage;
         pos[i] = c + (r - s.first_row[l[i]]);
         const int p = pos[i] / kPage;
-        const long long at = static_cast<long long>(head) + s.page0[l[i]] + (p - held);
+        const long long at = static_cast<long long>(head) + s.offset[l[i]] + (p - held);
         id[i] = p < held ? a.table[static_cast<size_t>(base + l[i]) * a.max_pages + p]
                          : a.ring[at < a.capacity ? at : at - a.capacity];
         if (id[i] < 0) flags |= KVTC_STATUS_BAD_PAGE;
@@ -250,13 +290,13 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const __grid_cons
       int32_t* row = a.table + static_cast<size_t>(base + i) * a.max_pages;
       if (need > 0) {
         for (int p = lane; p < need; p += 32) {
-          const long long at = static_cast<long long>(head) + s.page0[i] + p;
+          const long long at = static_cast<long long>(head) + s.offset[i] + p;
           row[held + p] = a.ring[at < a.capacity ? at : at - a.capacity];
         }
       } else if (need == -2) {
         for (int p = lane; p < held; p += 32) {
           const int32_t id = row[p];
-          const long long off = static_cast<long long>(s.release0[i]) + p;
+          const long long off = static_cast<long long>(s.offset[i]) + p;
           if (id < 0 || off >= room) flags |= KVTC_STATUS_BAD_PAGE;
           if (off < room) {
             const long long at = (static_cast<long long>(head) + count + off) % a.capacity;
@@ -356,11 +396,17 @@ extern "C" kvtc_status kvtc_step_tables(const int32_t* cached_lens, const int32_
   a.ticket = static_cast<int*>(workspace);
   a.status = status;
   const bool small = n_seq <= kSmallThreads;
+  const long long chunk = small ? kSmallThreads : static_cast<long long>(kLargeThreads) * kLargePer;
+  const bool narrow = chunk * std::max<long long>(n_rows + 1ll, max_pages) < (1ll << 31);  // sums fit an int
   const long long per_cta = kRowsPerThread * (small ? kSmallThreads : kLargeThreads);
-  const unsigned grid = static_cast<unsigned>(std::max<long long>(1, (n_rows + per_cta - 1) / per_cta));
-  const cudaError_t e = small ? raw::launch(step_tables_kernel<kSmallThreads, 1>, dim3(grid), kSmallThreads, 0, stream, a)
-                              : raw::launch(step_tables_kernel<kLargeThreads, kLargePer>, dim3(grid), kLargeThreads, 0,
-                                            stream, a);
+  const dim3 grid(static_cast<unsigned>(std::max<long long>(1, (n_rows + per_cta - 1) / per_cta)));
+  cudaError_t e;
+  if (small)
+    e = narrow ? raw::launch(step_tables_kernel<int, kSmallThreads, 1>, grid, kSmallThreads, 0, stream, a)
+               : raw::launch(step_tables_kernel<long long, kSmallThreads, 1>, grid, kSmallThreads, 0, stream, a);
+  else
+    e = narrow ? raw::launch(step_tables_kernel<int, kLargeThreads, kLargePer>, grid, kLargeThreads, 0, stream, a)
+               : raw::launch(step_tables_kernel<long long, kLargeThreads, kLargePer>, grid, kLargeThreads, 0, stream, a);
   if (e != cudaSuccess) return cuda_fail(e, "step tables launch");
   return KVTC_OK;
 }

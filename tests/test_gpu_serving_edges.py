@@ -323,3 +323,17 @@ def test_a_stream_handle_an_int_and_the_current_stream():
             kvtc.kvtc_raw_decode_attention(cache, 1, q, lens, 300, out, ws, stream=stream)
         side.synchronize()
         ref.assert_close(out, *ref.attention(q, *kv[0]))
+
+
+@pytest.mark.parametrize("n_seq,rows,max_pages", [(5, (1 << 24) + 3, 16), (130, 40, 1 << 20), (200, 1 << 20, 8)])
+def test_step_tables_whose_sums_may_pass_32_bits(n_seq, rows, max_pages):
+    # launches padded to very many rows and very wide tables: the scans run in 64 bits
+    cached, new, ring, state, table, _ = tables_case(n_seq, n_seq, 300, 3, 16, 2000, 0)
+    new[1] = (1 << 31) - 1
+    wide = np.full((n_seq, max_pages), -1, np.int32)
+    n = min(16, max_pages)
+    wide[:, :n] = table[:, :n]
+    case = (cached, new, ring, state, wide, rows)
+    got, want = run_tables(*case), ref.step_tables(*case)
+    assert want["status"] & kvtc.STATUS_BAD_POS
+    same_tables(got, want)
