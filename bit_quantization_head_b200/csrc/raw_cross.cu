@@ -92,7 +92,7 @@ struct Seq {
 struct __align__(1024) Smem {
   unsigned char q[2][kTileBytes];
   unsigned char kv[kStages][kTileBytes];
-  unsigned char out[2][4][4096];  // [tile][warp]: rows on their way out
+  unsigned char out[2][4][2048];  // [tile][warp]: rows on their way out
   Part part[2];
   uint64_t kv_full[kStages], kv_empty[kStages], q_full, q_empty, part_full[2], part_empty[2];
   uint64_t s_full[2], p_full[2][2], o_full[2], twin_full, twin_empty, drain;
@@ -580,6 +580,25 @@ __device__ __forceinline__ void put_rows(unsigned char* buf, uint16_t* out, int 
   }
 }
 
+// Takes a part (m, l, sums) in with what has been joined of its row; the reference moves on
+// from part to part, so that a part's reads are all under way at once.
+template <int N>
+__device__ __forceinline__ void join_part(float m, float l, const float4 (&v)[N], float c, float& top, float& sum,
+                                          bool& bad, float (&o)[4 * N]) {
+  const float to = fmaxf(top, m);
+  const float f0 = top == -INFINITY ? 0.0f : ex2((top - to) * c), f1 = m == -INFINITY ? 0.0f : ex2((m - to) * c);
+  bad |= l < 0.0f;
+  sum = sum * f0 + l * f1;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    o[4 * e] = o[4 * e] * f0 + v[e].x * f1;
+    o[4 * e + 1] = o[4 * e + 1] * f0 + v[e].y * f1;
+    o[4 * e + 2] = o[4 * e + 2] * f0 + v[e].z * f1;
+    o[4 * e + 3] = o[4 * e + 3] * f0 + v[e].w * f1;
+  }
+  top = to;
+}
+
 // Joins the parts of a tile of up to 32 rows: its four warps take 32 columns each of the same
 // rows (a row per thread left three of them idle: the first tokens of three answers over
 // 1500 states 21.4 us, 19.6 so), the CTA's own part with the others.
@@ -592,14 +611,6 @@ __device__ __forceinline__ void join_few(const CrossArgs& a, Smem& s, int tok0, 
   constexpr size_t kNext = 4 * kPartFloats;  // from a CTA's slot to the next CTA's
   float top = -INFINITY, sum = 0.0f, o[32];
   bool bad = false;
-#pragma unroll 4
-  for (int j = 0; j < shares; ++j) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(j == 0 ? first : second + (j - 1) * kNext) + lane);
-    if (live) {
-      top = fmaxf(top, ml.x);
-      bad |= ml.y < 0.0f;
-    }
-  }
 #pragma unroll
   for (int e = 0; e < 32; ++e) o[e] = 0.0f;
 #pragma unroll 2
@@ -609,12 +620,7 @@ __device__ __forceinline__ void join_few(const CrossArgs& a, Smem& s, int tok0, 
     float4 v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows) + (8 * q + e) * kRows + lane);
-    const float f = live && ml.x > -INFINITY ? ex2((ml.x - top) * a.c) : 0.0f;
-    if (live) sum += ml.y * f;
-    if (f > 0.0f)
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[4 * e] += v[e].x * f, o[4 * e + 1] += v[e].y * f, o[4 * e + 2] += v[e].z * f, o[4 * e + 3] += v[e].w * f;
+    if (live) join_part(ml.x, ml.y, v, a.c, top, sum, bad, o);
   }
   if (bad) {
 #pragma unroll
@@ -866,54 +872,33 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
           join_few<F16>(a, s, d.tok0 + x * a.tile_tok, d.head, rows, d.c0, shares);
         } else if (join) {
           __threadfence();
-          const int others = shares - 1, me = static_cast<int>(blockIdx.x) - d.c0;
-          auto other = [&](int i) { return d.c0 + i + (i >= me ? 1 : 0); };
           if (row == 0) *ticket = 0;
-          float top = m;
-          bool bad = d.bad;
-          float2* kept = reinterpret_cast<float2*>(s.out[x][warp & 3] + 2048) + lane;  // of the first 8
-          for (int i = 0; i < others; ++i) {
-            const int c = other(i);
-            const float2 ml = live ? __ldcg(reinterpret_cast<const float2*>(part_of(a, c, c == d.c0, x)) + row) : make_float2(0.0f, 0.0f);
-            top = fmaxf(top, ml.x);
-            bad |= ml.y < 0.0f;
-            if (i < 8) kept[32 * i] = ml;
-          }
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
-            float sum = 0.0f, o[64];
+            float top = -INFINITY, sum = 0.0f, o[64];
+            bool bad = false;
 #pragma unroll
             for (int e = 0; e < 64; ++e) o[e] = 0.0f;
 #pragma unroll 1
-            for (int j = 0; j < shares; ++j) {  // in order, whoever joins
-              if (j == me) {
-                const float f = m == -INFINITY ? 0.0f : ex2((m - top) * a.c);
-                sum += l * f;
+            for (int c = d.c0; c <= d.c1; ++c) {  // in order, whoever joins
+              float4 v[16];
+              float2 ml = make_float2(m, l);
+              if (c == static_cast<int>(blockIdx.x)) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                  float v[32];
-                  sums(2 * half + q, v);
-                  if (f > 0.0f)
+                  float w[32];
+                  sums(2 * half + q, w);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[32 * q + e] += v[e] * f;
+                  for (int e = 0; e < 8; ++e) v[8 * q + e] = make_float4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                 }
-                continue;
-              }
-              const int i = j - (j > me ? 1 : 0), c = d.c0 + j;
-              const float* p = part_of(a, c, c == d.c0, x);
-              float4 v[16];
-              if (live) {
+              } else if (live) {
+                const float* p = part_of(a, c, c == d.c0, x);
+                ml = __ldcg(reinterpret_cast<const float2*>(p) + row);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                   v[e] = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows) + (16 * half + e) * kRows + row);
-                const float2 ml = i < 8 ? kept[32 * i] : __ldcg(reinterpret_cast<const float2*>(p) + row);
-                const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
-                sum += ml.y * f;
-                if (f > 0.0f)
-#pragma unroll
-                  for (int e = 0; e < 16; ++e)
-                    o[4 * e] += v[e].x * f, o[4 * e + 1] += v[e].y * f, o[4 * e + 2] += v[e].z * f, o[4 * e + 3] += v[e].w * f;
               }
+              if (live) join_part(ml.x, ml.y, v, a.c, top, sum, bad, o);
             }
             if (bad) {
 #pragma unroll

@@ -256,33 +256,22 @@ __device__ __forceinline__ bool join_parts(const DecodeArgs& a, Smem<NT>& s, int
   __threadfence();
   if (tid == 0) *ticket = 0;
   for (int n = 0; n < NT && n * 8 < heads; ++n) {
-    // the largest reference of each head: 16 parts at a time
-    float top = -INFINITY;
-    bool any_bad = false;
-#pragma unroll 4
-    for (int i = tid >> 3; i < n_part; i += 16) {
-      const int c = first + i * step;
-      if (n * 8 + (tid & 7) < heads) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of<NT>(a, c, c == c0) + NT * 8 * kD + 2 * (n * 8 + (tid & 7))));
-        top = fmaxf(top, ml.x);
-        any_bad |= ml.y < 0.0f;
-      }
-    }
-    s.z[0][tid] = top;
-    s.z[1][tid] = any_bad ? 1.0f : 0.0f;
-    if (!sync()) return false;
     // a head's 16 chunks of 8 dims by 16 threads; with at most 4 heads the parts are dealt
-    // over the threads left (their sums are added in order)
+    // over the threads left (their sums are added in order).  The reference moves on from
+    // part to part, so that a part's reads are all under way at once.
     const int live = min(8, heads - n * 8), deal = live <= 1 ? 8 : live <= 2 ? 4 : live <= 4 ? 2 : 1, own = 8 / deal;
     const int slot = tid >> 4, hd = slot % own, sub = slot / own, row = n * 8 + hd, dim = (tid & 15) * 8;
-    float v[8] = {}, sum = 0.0f;
-    top = -INFINITY;
-    any_bad = false;
+    float v[8] = {}, sum = 0.0f, top = -INFINITY;
+    bool any_bad = false;
+    auto add = [&](float m, float l, const float (&x)[8]) {
+      const float to = fmaxf(top, m);
+      const float f0 = top == -INFINITY ? 0.0f : ex2((top - to) * a.c), f1 = m == -INFINITY ? 0.0f : ex2((m - to) * a.c);
+      any_bad |= l < 0.0f;
+      sum = sum * f0 + l * f1;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      top = fmaxf(top, s.z[0][8 * i + hd]);
-      any_bad |= s.z[1][8 * i + hd] != 0.0f;
-    }
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * f0 + x[e] * f1;
+      top = to;
+    };
     if (hd < live) {
 #pragma unroll 8
       for (int i = sub; i < n_part; i += deal) {
@@ -291,25 +280,26 @@ __device__ __forceinline__ bool join_parts(const DecodeArgs& a, Smem<NT>& s, int
         const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + NT * 8 * kD + 2 * row));
         const float4 x = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim));
         const float4 y = __ldcg(reinterpret_cast<const float4*>(p + row * kD + dim) + 1);
-        const float f = ml.x == -INFINITY ? 0.0f : ex2((ml.x - top) * a.c);
-        sum += ml.y * f;
-        v[0] += x.x * f, v[1] += x.y * f, v[2] += x.z * f, v[3] += x.w * f;
-        v[4] += y.x * f, v[5] += y.y * f, v[6] += y.z * f, v[7] += y.w * f;
+        const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        add(ml.x, ml.y, z);
       }
     }
-    if (!sync()) return false;
     if (deal > 1) {
       float* mine = s.z[0] + slot * kRowPad + dim;
 #pragma unroll
       for (int e = 0; e < 8; ++e) mine[e] = v[e];
-      if ((tid & 15) == 0) s.z[1][slot] = sum;
+      if ((tid & 15) == 0) {
+        s.z[1][2 * slot] = top;
+        s.z[1][2 * slot + 1] = any_bad ? -1.0f : sum;
+      }
       if (!sync()) return false;
       if (sub == 0) {
         for (int k = 1; k < deal; ++k) {
           const int from = hd + k * own;
-          sum += s.z[1][from];
+          float z[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += s.z[0][from * kRowPad + dim + e];
+          for (int e = 0; e < 8; ++e) z[e] = s.z[0][from * kRowPad + dim + e];
+          add(s.z[1][2 * from], s.z[1][2 * from + 1], z);
         }
       }
     }
@@ -485,35 +475,38 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
         s.l[warp][n * 8 + 2 * t + 1] = l[n][1];
       }
     }
-    if (!consumer_sync()) return;
     const int slot = d.flags & kBegins ? 1 : 0;
     const size_t out0 = static_cast<size_t>(d.seq) * a.H * a.G + static_cast<size_t>(h) * a.G + grp * a.group_heads;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n * 8 >= heads) break;
-      float f[2];
+      // (z0 + z2) + (z1 + z3): warps 0 and 1 leave their sums as they are, 2 and 3 scale both
+      float* mine = s.z[warp & 1] + 2 * t * kRowPad + g;
+      if (warp < 2) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int hd = n * 8 + 2 * t + j;
-        const float top = fmaxf(fmaxf(s.m[0][hd], s.m[1][hd]), fmaxf(s.m[2][hd], s.m[3][hd]));
-        f[j] = m[n][j] == -INFINITY ? 0.0f : ex2((m[n][j] - top) * a.c);
+        for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mine[(e & 1) * kRowPad + 16 * mt + (e >> 1) * 8] = z[n][mt][e];
       }
-      // (z0 + z2) + (z1 + z3), whatever the warps' order
+      if (!consumer_sync()) return;
+      if (warp >= 2) {
+        float f[2], f0[2];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (warp >> 1 == w) {
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float* p = s.z[warp & 1] + (2 * t + (e & 1)) * kRowPad + 16 * mt + (e >> 1) * 8 + g;
-              const float v = z[n][mt][e] * f[e & 1];
-              *p = w == 0 ? v : *p + v;
-            }
-          }
+        for (int j = 0; j < 2; ++j) {
+          const int hd = n * 8 + 2 * t + j;
+          const float top = fmaxf(fmaxf(s.m[0][hd], s.m[1][hd]), fmaxf(s.m[2][hd], s.m[3][hd])), m0 = s.m[warp - 2][hd];
+          f[j] = m[n][j] == -INFINITY ? 0.0f : ex2((m[n][j] - top) * a.c);
+          f0[j] = m0 == -INFINITY ? 0.0f : ex2((m0 - top) * a.c);
         }
-        if (!consumer_sync()) return;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float* p = mine + (e & 1) * kRowPad + 16 * mt + (e >> 1) * 8;
+            *p = *p * f0[e & 1] + z[n][mt][e] * f[e & 1];
+          }
       }
+      if (!consumer_sync()) return;
       const int hd = tid >> 4, dim = (tid & 15) * 8, row = n * 8 + hd;
       if (row < heads) {
         float top = -INFINITY, sum = 0.0f;
