@@ -304,9 +304,10 @@ __device__ void load_role(const CrossArgs& a, Smem& s, const CUtensorMap* kv_map
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (bad_seq && blockIdx.x == 0 && a.status) atomicOr(a.status, static_cast<int>(KVTC_STATUS_BAD_POS));
   // Runs of r steps take r steps and join up to longest / r parts at the end of a unit, a
-  // part costing about two steps of a small call: no run shorter than sqrt(2 longest) (one
-  // 20000-token sequence: 38 us, 44 with sqrt(longest / 2), 42 with sqrt(4 longest)).
-  const int shortest = max(1, static_cast<int>(sqrtf(2.0f * static_cast<float>(longest))));
+  // part costing about a step of a small call: no run shorter than sqrt(longest) (3 queries
+  // over 20000 states: 34.9 us, 38.6 with sqrt(longest / 2), 39.4 with sqrt(4 longest); 4
+  // over 8000: 19.8, 21.7 with sqrt(2 longest)).
+  const int shortest = max(1, static_cast<int>(sqrtf(static_cast<float>(longest))));
   const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), divide(total + shortest - 1, shortest)));
   long long f = 0, f1 = 0;
   if (static_cast<int>(blockIdx.x) < n_cta) {
