@@ -444,14 +444,17 @@ __device__ void mma_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
     for (int kk = 0; kk < 8; ++kk) mma_ss(d, q + step_k(kk), k + step_k(kk), idesc<F16>(false), kk > 0, one);
     tc_commit(&s.s_full[x], one);
   };
-  // O_x += P_x V for the first `groups` groups of 16 tokens, each half of P as it arrives
-  auto values = [&](int x, int i, bool acc, int groups) -> bool {
+  // O_x += P_x V for the first `groups` groups of 16 tokens, each half of P as it arrives; in
+  // between, while the row warps work on the second, tile `next` of the ring is waited for
+  // (-1: none), which the scores that follow need.
+  auto values = [&](int x, int i, bool acc, int groups, int next) -> bool {
     const uint32_t d = tmem + 256 + x * 128, p = tmem + x * 128, v = v0 + (i & (kStages - 1)) * (kTileBytes >> 4);
     if (!wait(&s.p_full[x][0], p_phase[x])) return false;
     tc_fence_after();
     if (groups == 8) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) mma_ts(d, p + 8 * g, v + step_n(g), idesc<F16>(true), acc || g > 0, one);
+      if (next >= 0 && !loaded(next)) return false;
       if (!wait(&s.p_full[x][1], p_phase[x])) return false;
       tc_fence_after();
 #pragma unroll
@@ -495,16 +498,13 @@ __device__ void mma_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
         const int v = it + 2 * j + 1, k = v + 1;
         const bool more = j + 1 < steps;
         const int groups = more ? 8 : last_groups;
-        if (!(ok = loaded(v) && values(0, v, j > 0, groups))) break;
-        if (more) {
-          if (!(ok = loaded(k))) break;
-          tc_fence_after();
+        if (!(ok = loaded(v) && values(0, v, j > 0, groups, more ? k : -1))) break;
+        if (more)
           scores(0, 0, k);
-        } else {
+        else
           tc_commit(&s.o_full[0], one);
-        }
         if (two) {
-          if (!(ok = values(1, v, j > 0, groups))) break;
+          if (!(ok = values(1, v, j > 0, groups, -1))) break;
           if (more)
             scores(1, 1, k);
           else
@@ -517,7 +517,8 @@ __device__ void mma_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
     } else {
       for (int j = 0; j < steps; ++j) {
         const int x = j & 1, v = it + 2 * j + 1, k = v + 3;
-        if (!(ok = loaded(v) && values(x, v, j > 1, j + 1 < steps ? 8 : last_groups))) break;
+        // (the next K tile of a twin part is often still on its way: not waited for early)
+        if (!(ok = loaded(v) && values(x, v, j > 1, j + 1 < steps ? 8 : last_groups, -1))) break;
         release(v);
         if (j + 2 < steps) {
           if (!(ok = loaded(k))) break;
