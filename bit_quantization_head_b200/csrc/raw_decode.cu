@@ -8,8 +8,8 @@
 // runs as m16n8k16 MMAs (scores: 16 tokens x 8 heads; values: 16 dims x 8 heads).  Measured:
 // 16 x 32768 tokens of 8 KV heads in 331 us (6.5 TB/s, the rate of a copy), one sequence of
 // 131072 tokens and 4 KV heads in 56 us (41 at that rate: about 4 us until the first tiles
-// are there, 6 to join 74 parts of a head), 4096 tokens in 11.4 us and three chats of up to
-// 1000 tokens in 9.5 us (launch, two dependent reads, a tile, and the join of its parts).
+// are there, 6 to join 74 parts of a head), 4096 tokens in 10.8 us and three chats of up to
+// 1000 tokens in 8.9 us (launch, two dependent reads, a tile, and the join of its parts).
 //
 // Work split.  A unit is (sequence, KV head, group of query heads), its tiles 64 tokens.  All
 // tiles of all units in a row are cut into one equal run per CTA (2 CTAs per SM), whatever
