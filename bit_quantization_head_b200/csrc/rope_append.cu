@@ -15,7 +15,7 @@
 // for one another (a block of a few tokens that shared them behind a barrier reached 3.3 TB/s,
 // at two blocks per SM).  Few tokens: a token's rows are dealt over several warps.  Measured:
 // 32768 bf16 tokens of 40 heads in 102 us (6.6 TB/s, the rate of a copy), 16411 tokens into
-// pages in 64.5 us (6.3 TB/s), 16 tokens in 3.2 us.
+// pages in 64.5 us (6.3 TB/s), 4097 fp32 tokens of 32 heads in 20.9 us, 16 tokens in 3.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,8 +34,17 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHalf = kD / 2;
-constexpr int kBatch = 4;            // rows of a lane in flight
-constexpr int kBusyWarps = 148 * 48;  // two rounds of warps on every SM: one of 1.15 left a tail (4097 fp32 rows of 32 heads 26.6 us, two 23.9, eight 31.7)
+// Rows of a lane in flight, and blocks per SM: 4 and 3 in 16 bits (32768 tokens 102.5 us, 104.3
+// with 2 and 4), 2 and 4 in fp32 (4097 tokens of 32 heads, two warps a token: 21.6 us, 23.9
+// with 4 and 3).
+template <typename T>
+constexpr int kBatchOf = sizeof(T) == 4 ? 2 : 4;
+template <typename T>
+constexpr int kBlocksOf = sizeof(T) == 4 ? 4 : 3;
+// Warps from which a token has no more than one: every further warp of a token makes its
+// sines again (2000 tokens of 40 heads 9.8 us with 12 or less per SM, 10.0 with 24, 12.8 with
+// 48; 300 tokens 4.6 with 12, 5.5 with 24).
+constexpr int kBusyWarps = 148 * 12;
 
 struct RopeArgs {
   const void* x[3];        // q, k, v (null: absent)
@@ -70,11 +79,12 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocksOf<T>) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));  // elements of a 16-byte chunk
   constexpr int kPer = kVec / 4;                           // elements of a 32-bit word
   constexpr int kLanes = kHalf / kVec;                     // lanes of a row
   constexpr int kRows = 32 / kLanes;                       // rows moved at a time
+  constexpr int kBatch = kBatchOf<T>;
   __shared__ float2 cs[kWarps][kHalf];
   griddep_wait();
   griddep_launch_dependents();
@@ -220,7 +230,7 @@ kvtc_status check_rope_overlap(const RopeArgs& a, size_t es, const kvtc_raw_cach
 }
 
 kvtc_status launch_rope(RopeArgs& a, kvtc_dtype dtype, void* stream) {
-  // as many warps of a token as fill the chip, each with one batch of loads at least
+  // as many warps of a token as keep the chip busy, each with some rows at least
   const int at_once = dtype == KVTC_F32 ? 2 : 4;  // rows a warp moves at a time
   const int n_all = a.heads[0] + a.heads[1] + a.heads[2];
   const int most = (n_all + at_once - 1) / at_once;
