@@ -9,7 +9,7 @@
 // 16 x 32768 tokens of 8 KV heads in 331 us (6.5 TB/s, the rate of a copy), one sequence of
 // 131072 tokens and 4 KV heads in 56 us (41 at that rate: about 4 us until the first tiles
 // are there, 6 to join 74 parts of a head), 4096 tokens in 10.8 us and three chats of up to
-// 1000 tokens in 8.9 us (launch, two dependent reads, a tile, and the join of its parts).
+// 1000 tokens in 8.6 us (launch, two dependent reads, a tile, and the join of its parts).
 //
 // Work split.  A unit is (sequence, KV head, group of query heads), its tiles 64 tokens.  All
 // tiles of all units in a row are cut into one equal run per CTA (2 CTAs per SM), whatever
@@ -133,7 +133,7 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
   SlotScan<decltype(tiles)> scan(a.n_seq, tiles);
   const long long total = scan.total;
   // Runs of at least 1 to 4 tiles: fewer parts to join where one sequence has the chip (4096
-  // tokens of 8 heads: 11.4 us with 4, 12.8 with 1; 1000 tokens: 9.5 with 1, 10.9 with 2).
+  // tokens of 8 heads: 10.4 us with 4, 11.8 with 1; 1000 tokens: 7.8 with 1, 8.5 with 2).
   const int shortest = min(4, max(1, __reduce_max_sync(0xffffffffu, longest) / 16));
   const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), divide(total + shortest - 1, shortest)));
   long long f = 0, f1 = 0, base = 0;  // base: first tile of the sequence's units
@@ -161,7 +161,7 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
     const int i0 = static_cast<int>(f - base - static_cast<long long>(u) * nt);
     const int i1 = static_cast<int>(min(static_cast<long long>(nt), i0 + (f1 - f)));
     const long long begin = base + static_cast<long long>(u) * nt;
-    const int c0 = run_owner(begin, n_cta, total), c1 = run_owner(begin + nt - 1, n_cta, total);
+    int c0 = 0, c1 = 0;
     const int h = u / a.groups, grp = u - h * a.groups;
     const int heads = min(a.group_heads, a.G - grp * a.group_heads);
     for (int i = i0; i < i1 && ok; ++i, ++it) {
@@ -179,6 +179,23 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
       if (lane == 0) {
         if (it >= stages(NT)) ok = wait_phase(&s.empty[st], (it / stages(NT) - 1) & 1, dead);
         if (ok) {
+          // The copies first, what the consumers read beside them while they fly: the phase
+          // cannot end before the arrival below (4096 tokens of 8 heads: 10.7 -> 10.4 us).
+          if (good) {
+            const int row = a.row0 + (id * a.H + h) * 2 * kPage + (i * kTile) % kPage;
+            unsigned char* dst = s.kv[st];
+            tma_load_2d(dst, map, 0, row, &s.full[st]);
+            tma_load_2d(dst + kBoxBytes, map, 64, row, &s.full[st]);
+            tma_load_2d(dst + 2 * kBoxBytes, map, 0, row + kPage, &s.full[st]);
+            tma_load_2d(dst + 3 * kBoxBytes, map, 64, row + kPage, &s.full[st]);
+          }
+          const uint32_t q_bytes = i == i0 ? static_cast<uint32_t>(heads) * 256u : 0u;
+          if (q_bytes) {
+            bulk_copy_g2s(s.q[st], a.q + (static_cast<size_t>(seq) * a.H * a.G + static_cast<size_t>(h) * a.G + grp * a.group_heads) * kD,
+                          q_bytes, &s.full[st]);
+            c0 = run_owner(begin, n_cta, total);
+            c1 = run_owner(begin + nt - 1, n_cta, total);
+          }
           TileDesc& d = s.desc[st];
           d.n = good ? min(kTile, len - i * kTile) : 0;
           d.flags = (i == i0 ? kFirst : 0) | (i == i1 - 1 ? kLast : 0) | (have && !good ? kBad : 0) |
@@ -188,19 +205,7 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
           d.head = u;
           d.c0 = c0;
           d.c1 = c1;
-          const uint32_t q_bytes = i == i0 ? static_cast<uint32_t>(heads) * 256u : 0u;
           mbar_arrive_expect_tx(&s.full[st], (good ? kTileBytes : 0u) + q_bytes);
-          if (good) {
-            const int row = a.row0 + (id * a.H + h) * 2 * kPage + (i * kTile) % kPage;
-            unsigned char* dst = s.kv[st];
-            tma_load_2d(dst, map, 0, row, &s.full[st]);
-            tma_load_2d(dst + kBoxBytes, map, 64, row, &s.full[st]);
-            tma_load_2d(dst + 2 * kBoxBytes, map, 0, row + kPage, &s.full[st]);
-            tma_load_2d(dst + 3 * kBoxBytes, map, 64, row + kPage, &s.full[st]);
-          }
-          if (q_bytes)
-            bulk_copy_g2s(s.q[st], a.q + (static_cast<size_t>(seq) * a.H * a.G + static_cast<size_t>(h) * a.G + grp * a.group_heads) * kD,
-                          q_bytes, &s.full[st]);
         }
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
