@@ -709,8 +709,12 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
           }
           fence_proxy_async_smem();
         }
-        if (__any_sync(0xffffffffu, (top - m) * a.c > kSlack)) {
-          const float to_m = fmaxf(m, top);
+        // Each row decides for itself (the others are scaled by 1): rows of the warp that belong
+        // to another sequence, or to none (heads that do not fill 128 rows, whose queries no load
+        // writes), must not change the bits of these.
+        const bool moves = (top - m) * a.c > kSlack;
+        if (__any_sync(0xffffffffu, moves)) {
+          const float to_m = moves ? top : m;
           const float f = m == -INFINITY ? 0.0f : ex2((m - to_m) * a.c);
           l *= f;
           m = to_m;
