@@ -258,13 +258,14 @@ __device__ __forceinline__ Seq seq_of(const CrossArgs& a, int s) {
 
 // 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer, 2^f by a polynomial
 // (minimax in relative error on [-1/2, 1/2], fitted for this kernel: 2^-13.7 for bf16
-// weights, 2^-18.5 for fp16), times 2^n.  x is held above -126; NaN stays NaN.
+// weights, 2^-18.5 for fp16), times 2^n.  x is held above -127, whose 2^n comes out as 0 (a
+// score of -inf, and one past the end, weighs nothing); NaN stays NaN.
 template <bool F16>
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
   float a, b;
   unpair(x, a, b);
-  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(a) : "f"(-126.0f));
-  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(b) : "f"(-126.0f));
+  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(a) : "f"(-127.0f));
+  asm("max.NaN.f32 %0, %0, %1;\n" : "+f"(b) : "f"(-127.0f));
   x = pair(a, b);
   const uint64_t t = add2(x, pair(12582912.0f, 12582912.0f));  // 1.5 * 2^23 + n
   const uint64_t n = add2(t, pair(-12582912.0f, -12582912.0f));
@@ -733,7 +734,8 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
             }
           }
         }
-        const float neg = kBias - m * a.c;
+        // (a row without a score above -inf yet: their weights are 2^-inf, not 2^(inf - inf))
+        const float neg = m == -INFINITY ? 0.0f : kBias - m * a.c;
         const uint64_t neg2 = pair(neg, neg);
         uint64_t sum0 = pair(0.0f, 0.0f), sum1 = sum0;
         // The scores are read from TMEM once more, 64 columns at a time in one piece of code:
@@ -811,8 +813,8 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
         if (both) {
           const float2 ml = s.twin_ml[row];
           const float to_m = fmaxf(m, ml.x);
-          fa = ex2((m - to_m) * a.c);
-          fb = ex2((ml.x - to_m) * a.c);
+          fa = m == -INFINITY ? 0.0f : ex2((m - to_m) * a.c);
+          fb = ml.x == -INFINITY ? 0.0f : ex2((ml.x - to_m) * a.c);
           m = to_m;
           l = l * fa + ml.y * fb;
         }
@@ -839,6 +841,7 @@ __device__ void row_role(const CrossArgs& a, Smem& s, uint32_t tmem) {
         }
       };
       if (whole) {
+        // (a row whose every score is -inf has no softmax: 0 / 0, here as in the joins)
         const float r = some ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
