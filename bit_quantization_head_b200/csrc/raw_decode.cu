@@ -46,6 +46,9 @@ constexpr uint32_t kBoxBytes = kTile * 128;        // 64 tokens x 64 elements
 constexpr uint32_t kTileBytes = 4 * kBoxBytes;     // K, V x two halves
 constexpr int kMaxCtas = 320;                      // partial slots in the workspace
 constexpr int kRowPad = 132;                       // floats of a scratch row (conflict-free)
+// Reference of a head that has met no score above -inf: a weight is then 2^(-inf - it) = 0
+// where 2^(-inf - -inf) would be NaN, and its sums are 0, so any factor serves a join.
+constexpr float kLowest = -3.402823466e38f;
 
 __host__ __device__ constexpr int stages(int nt) { return nt == 1 ? 3 : 5; }
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
@@ -226,10 +229,10 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
 }
 
 // ------------------------------------------------------------------ consumer warps
-// One query head's 8 dims of a finished sum.
+// One query head's 8 dims of a finished sum (r: 1 / l; where every score is -inf that makes
+// 0 / 0, a row without a softmax, and 0 where there is nothing to attend to).
 template <bool F16>
-__device__ __forceinline__ void store_out(uint16_t* dst, const float (&z)[8], float l) {
-  const float r = l > 0.0f ? 1.0f / l : 0.0f;
+__device__ __forceinline__ void store_out(uint16_t* dst, const float (&z)[8], float r) {
   uint4 w;
   w.x = pack2<F16>(z[0] * r, z[1] * r);
   w.y = pack2<F16>(z[2] * r, z[3] * r);
@@ -266,11 +269,11 @@ __device__ __forceinline__ bool join_parts(const DecodeArgs& a, Smem<NT>& s, int
     // part to part, so that a part's reads are all under way at once.
     const int live = min(8, heads - n * 8), deal = live <= 1 ? 8 : live <= 2 ? 4 : live <= 4 ? 2 : 1, own = 8 / deal;
     const int slot = tid >> 4, hd = slot % own, sub = slot / own, row = n * 8 + hd, dim = (tid & 15) * 8;
-    float v[8] = {}, sum = 0.0f, top = -INFINITY;
+    float v[8] = {}, sum = 0.0f, top = kLowest;
     bool any_bad = false;
     auto add = [&](float m, float l, const float (&x)[8]) {
       const float to = fmaxf(top, m);
-      const float f0 = top == -INFINITY ? 0.0f : ex2((top - to) * a.c), f1 = m == -INFINITY ? 0.0f : ex2((m - to) * a.c);
+      const float f0 = ex2((top - to) * a.c), f1 = ex2((m - to) * a.c);
       any_bad |= l < 0.0f;
       sum = sum * f0 + l * f1;
 #pragma unroll
@@ -314,7 +317,7 @@ __device__ __forceinline__ bool join_parts(const DecodeArgs& a, Smem<NT>& s, int
         for (int e = 0; e < 8; ++e) v[e] = 0.0f;
       }
       if (kFinal) {
-        store_out<F16>(a.out + (out0 + row) * kD + dim, v, any_bad ? 0.0f : sum);
+        store_out<F16>(a.out + (out0 + row) * kD + dim, v, any_bad ? 0.0f : 1.0f / sum);
       } else {
         float* p = part_of<NT>(a, first, first == c0);
         reinterpret_cast<float4*>(p + row * kD + dim)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -356,7 +359,7 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
   const int kch = lane >> 4, vch = (lane >> 3) & 1;
   uint32_t qf[NT][8][2];
   float z[NT][8][4], m[NT][2], l[NT][2];
-  bool bad = false;
+  bool bad = false, some = false;  // of the unit's tiles so far: a bad page, tokens
   auto consumer_sync = [&]() -> bool { return consumers_sync(1, 32 * kConsumers, dead); };
   for (int it = 0;; ++it) {
     const int st = it % stages(NT);
@@ -374,7 +377,7 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
     const int h = d.head / a.groups, grp = d.head - h * a.groups;
     const int heads = min(a.group_heads, a.G - grp * a.group_heads);
     if (d.flags & kFirst) {
-      bad = false;
+      bad = some = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const bool live = n * 8 + g < heads;
@@ -385,11 +388,12 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
           qf[n][ks][1] = live ? row[8 * ks + 4 + t] : 0u;
           z[n][ks][0] = z[n][ks][1] = z[n][ks][2] = z[n][ks][3] = 0.0f;
         }
-        m[n][0] = m[n][1] = -INFINITY;
+        m[n][0] = m[n][1] = kLowest;
         l[n][0] = l[n][1] = 0.0f;
       }
     }
     bad |= (d.flags & kBad) != 0;
+    some |= d.n > 0;
     const int nv = d.n - 16 * warp;
     if (nv > 0) {
       const uint32_t tile = smem_u32(s.kv[st]);
@@ -500,8 +504,8 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
         for (int j = 0; j < 2; ++j) {
           const int hd = n * 8 + 2 * t + j;
           const float top = fmaxf(fmaxf(s.m[0][hd], s.m[1][hd]), fmaxf(s.m[2][hd], s.m[3][hd])), m0 = s.m[warp - 2][hd];
-          f[j] = m[n][j] == -INFINITY ? 0.0f : ex2((m[n][j] - top) * a.c);
-          f0[j] = m0 == -INFINITY ? 0.0f : ex2((m0 - top) * a.c);
+          f[j] = ex2((m[n][j] - top) * a.c);
+          f0[j] = ex2((m0 - top) * a.c);
         }
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt)
@@ -514,12 +518,11 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
       if (!consumer_sync()) return;
       const int hd = tid >> 4, dim = (tid & 15) * 8, row = n * 8 + hd;
       if (row < heads) {
-        float top = -INFINITY, sum = 0.0f;
+        float top = kLowest, sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, s.m[w][row]);
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w)
-          sum += s.m[w][row] == -INFINITY ? 0.0f : s.l[w][row] * ex2((s.m[w][row] - top) * a.c);
+        for (int w = 0; w < kConsumers; ++w) sum += s.l[w][row] * ex2((s.m[w][row] - top) * a.c);
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = s.z[0][hd * kRowPad + dim + e] + s.z[1][hd * kRowPad + dim + e];
@@ -528,7 +531,7 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0.0f;
           }
-          store_out<F16>(a.out + (out0 + row) * kD + dim, v, bad ? 0.0f : sum);
+          store_out<F16>(a.out + (out0 + row) * kD + dim, v, bad || !some ? 0.0f : 1.0f / sum);
         } else {
           float* p = part_of<NT>(a, blockIdx.x, slot);
           reinterpret_cast<float4*>(p + row * kD + dim)[0] = make_float4(v[0], v[1], v[2], v[3]);

@@ -508,7 +508,9 @@ uint64_t kvtc_raw_cross_workspace_bytes(int n_seq, int n_tok, int n_q_heads, int
  * calls of this function that fit it, but calls that share a workspace and overlap on the
  * GPU race (after KVTC_STATUS_TIMEOUT it must be zero-filled again).  The weights enter the
  * product with V in the cache's type; a NaN among the keys or values read shows in the rows
- * that read it, slots behind seq_lens[s] never do.  At most 1024 query heads per KV head.
+ * that read it, slots behind seq_lens[s] never do.  A score of -inf weighs nothing; a row with
+ * a score of +inf, or whose every score is -inf, has no softmax and is NaN.  At most 1024
+ * query heads per KV head.
  */
 kvtc_status kvtc_raw_decode_attention(const kvtc_raw_cache* cache, int layer, const void* q, int n_q_heads,
                                       const int32_t* seq_lens, int max_seq_len, float softmax_scale, void* out,

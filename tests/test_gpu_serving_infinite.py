@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests import serving_reference as ref
-from tests.test_gpu_serving import cross, states
+from tests.test_gpu_serving import cross, decode, states
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -42,6 +42,53 @@ def check(out, q, kv, keep, g):
     k, v = kv
     ref.assert_close(out[:, :g], *ref.attention(q[:, :g], k[:, :1], v[:, :1]))
     ref.assert_close(out[:, g:], *ref.attention(q[:, g:], k[keep, 1:], v[keep, 1:]))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("g", [3, 8, 12])
+@pytest.mark.parametrize("n,masked", CASES)
+def test_decode_gives_a_score_of_minus_infinity_no_weight(n, masked, g, dtype):
+    cache, kv, keep = cache_of(n, masked, dtype, 11)
+    q = queries(2, 2 * g, dtype, 12)
+    out = decode(cache, 1, q, [n, 130])
+    check(out[:1], q[:1], kv[0], keep, g)
+    ref.assert_close(out[1:], *ref.attention(q[1:], *kv[1]))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [1, 20, 128, 300, 9000])
+@pytest.mark.parametrize("value", [-INF, INF])
+def test_decode_rows_without_a_softmax_are_nan_and_alone(n, value, dtype):
+    g = 4
+    cache, kv = states([n, 130], 2, dtype, 15)
+    k, v = kv[0]
+    k = k.clone()
+    k[:, 1, 5] = -INF                   # every score of KV head 1 is -inf ..
+    if value == INF:
+        k[n // 2, 1, 5] = INF           # .. but for one of +inf
+    ref.scatter_states(cache.pool, 1, cache.block_table, 0, k, v)
+    q = queries(2, 2 * g, dtype, 16)
+    out = decode(cache, 1, q, [n, 130])
+    assert out[0, g:].isnan().all()
+    ref.assert_close(out[:1, :g], *ref.attention(q[:1, :g], k[:, :1], v[:, :1]))
+    ref.assert_close(out[1:], *ref.attention(q[1:], *kv[1]))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_decode_heads_of_one_kv_head_that_score_differently(dtype):
+    n, g = 200, 8
+    cache, kv = states([n, 130], 2, dtype, 17)
+    k, v = kv[0]
+    k = k.clone()
+    k[:100, 1, 5] = -INF
+    ref.scatter_states(cache.pool, 1, cache.block_table, 0, k, v)
+    q = queries(2, 2 * g, dtype, 18)
+    q[:, 1::2, 5] *= -1.0
+    keep = torch.arange(n, device="cuda") >= 100
+    out = decode(cache, 1, q, [n, 130])[:1]
+    assert out[:, g + 1::2].isnan().all()
+    ref.assert_close(out[:, :g:2], *ref.attention(q[:1, :g:2], k[:, :1], v[:, :1]))
+    ref.assert_close(out[:, g::2], *ref.attention(q[:1, g::2], k[keep, 1:], v[keep, 1:]))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
