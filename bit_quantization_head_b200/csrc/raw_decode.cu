@@ -311,6 +311,9 @@ __device__ __forceinline__ bool join_parts(const DecodeArgs& a, Smem<NT>& s, int
         }
       }
     }
+    // a part's result may go to the place of the first part: all of a head's threads, which are
+    // of one warp, have read that one's (m, l) by then
+    __syncwarp();
     if (sub == 0 && hd < live) {
       if (any_bad) {
 #pragma unroll

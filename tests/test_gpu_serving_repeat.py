@@ -4,7 +4,8 @@ other calls have used the chip, from another place in memory, and beside other r
 import pytest
 import torch
 
-from tests.test_gpu_serving import cross, decode, states
+from bit_quantization_head_b200 import kvtc
+from tests.test_gpu_serving import cross, decode, i32, states
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -63,3 +64,16 @@ def test_the_same_bits_every_time_and_everywhere(lens, q_lens, hq, hk, dtype):
         got = decode(cache, 1, qd, lens), cross(cache, 1, qx, q_lens, lens)
         first = first or got
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+def test_decode_joins_groups_of_parts_the_same_way_every_time():
+    # more than 48 parts of 5 to 8 heads: groups of parts are joined into the place of their first
+    for hq in (5, 8):
+        cache, _ = states([60000], 1, torch.bfloat16, 10)
+        q, sl = rand_q(1, hq, torch.bfloat16, 11), i32([60000])
+        ws = torch.zeros(kvtc.kvtc_raw_decode_workspace_bytes(1, hq, 1, 60000), dtype=torch.uint8, device="cuda")
+        outs = [torch.empty_like(q) for _ in range(200)]
+        for out in outs:
+            kvtc.kvtc_raw_decode_attention(cache, 1, q, sl, 60000, out, ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, outs[0]) for out in outs)
