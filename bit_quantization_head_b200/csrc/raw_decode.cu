@@ -174,7 +174,8 @@ __device__ void produce(const DecodeArgs& a, Smem<NT>& s, const CUtensorMap* map
         page_seq = seq;
         page0 = page;
         const int p = page + lane;
-        page_id = p * kPage < len ? a.table[static_cast<size_t>(seq) * a.max_pages + p] : -1;
+        // (in pages: p * 128 passes 31 bits behind the last page of the longest table)
+        page_id = p < (len + kPage - 1) / kPage ? a.table[static_cast<size_t>(seq) * a.max_pages + p] : -1;
       }
       const int id = __shfl_sync(0xffffffffu, page_id, len > 0 ? page - page0 : 0);
       const bool have = len > 0, good = have && id >= 0 && id < a.n_pages;
