@@ -111,8 +111,11 @@ __global__ void __launch_bounds__(128) encode_append_kernel(const __grid_constan
       else
         hi = mid - 1;
     }
-    s_seq = lo;
-    s_pos = static_cast<long long>(a.pos_start[lo]) + (tok - a.cu_seqlens[lo]);
+    const int c0 = a.cu_seqlens[lo], c1 = a.cu_seqlens[lo + 1];
+    if (c0 <= tok && tok < c1) {
+      s_seq = lo;
+      s_pos = static_cast<long long>(a.pos_start[lo]) + (tok - c0);
+    }
   }
   xs[j] = xv;
   __syncthreads();

@@ -240,7 +240,8 @@ uint64_t kvtc_unit_pool_offset(const kvtc_plan* plan, int unit, uint64_t pages_p
  * cu_seqlens[n_seq] = n_tok).  pos_start: device int32 [n_seq], cache position of each
  * sequence's first new token.  The slots written are overwritten (their old bits are
  * cleared, other tokens sharing a 32-bit word are kept).  Positions beyond
- * max_pages * 128 or page ids outside the pool set status bits and are skipped.
+ * max_pages * 128, rows that no sequence holds (KVTC_STATUS_BAD_POS) or page ids outside the
+ * pool set status bits and are skipped.
  * Calls that write the same slot and overlap on the GPU race.  An uncompressed value unit
  * (KVTC_RAW_BITS) receives fp16(v) (round to nearest even) in its raw page layout.
  */
