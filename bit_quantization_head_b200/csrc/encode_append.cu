@@ -32,6 +32,7 @@ struct AppendArgs {
   uint64_t pages_per_unit;
   const int32_t* block_table;
   int max_pages;
+  const int64_t* slots;  // kvtc_encode_append_slots: page * 128 + token of the page, per row
   int32_t* status;
 };
 
@@ -60,7 +61,9 @@ __device__ __forceinline__ void store_code(uint32_t* page, int kind, int r, int 
 
 // CTA = (token, unit of the layer); thread j computes coordinate j.  The token's row is
 // staged in shared memory once; each thread holds its row of M in registers; the fma
-// chains then run in the canonical order from registers and broadcast reads.
+// chains then run in the canonical order from registers and broadcast reads.  kSlots: the
+// rows' places are given, instead of being looked up by sequence and position.
+template <bool kSlots>
 __global__ void __launch_bounds__(128) encode_append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ float xs[kD];
   __shared__ int s_seq;
@@ -88,45 +91,54 @@ __global__ void __launch_bounds__(128) encode_append_kernel(const __grid_constan
   // round of loads finds it; more sequences than threads take a binary search).
   const float xv = a.bf16 ? __bfloat162float((static_cast<const __nv_bfloat16*>(kind ? a.v : a.k) + xoff)[j])
                           : (static_cast<const float*>(kind ? a.v : a.k) + xoff)[j];
-  if (j == 0) {  // (a token no interval holds is reported as a bad position)
-    s_seq = 0;
-    s_pos = -1;
-  }
-  __syncthreads();
-  if (a.n_seq <= static_cast<int>(blockDim.x)) {
-    if (j < a.n_seq) {
-      const int c0 = a.cu_seqlens[j], c1 = a.cu_seqlens[j + 1];
-      const int ps = a.pos_start[j];
-      if (c0 <= tok && tok < c1) {
-        s_seq = j;
-        s_pos = static_cast<long long>(ps) + (tok - c0);
+  const long long place = kSlots ? a.slots[tok] : 0;
+  if (kSlots && place < 0) return;  // (the whole block: a row that goes nowhere)
+  if constexpr (!kSlots) {
+    if (j == 0) {  // (a token no interval holds is reported as a bad position)
+      s_seq = 0;
+      s_pos = -1;
+    }
+    __syncthreads();
+    if (a.n_seq <= static_cast<int>(blockDim.x)) {
+      if (j < a.n_seq) {
+        const int c0 = a.cu_seqlens[j], c1 = a.cu_seqlens[j + 1];
+        const int ps = a.pos_start[j];
+        if (c0 <= tok && tok < c1) {
+          s_seq = j;
+          s_pos = static_cast<long long>(ps) + (tok - c0);
+        }
       }
-    }
-  } else if (j == 0) {
-    int lo = 0, hi = a.n_seq - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.cu_seqlens[mid] <= tok)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const int c0 = a.cu_seqlens[lo], c1 = a.cu_seqlens[lo + 1];
-    if (c0 <= tok && tok < c1) {
-      s_seq = lo;
-      s_pos = static_cast<long long>(a.pos_start[lo]) + (tok - c0);
+    } else if (j == 0) {
+      int lo = 0, hi = a.n_seq - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.cu_seqlens[mid] <= tok)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int c0 = a.cu_seqlens[lo], c1 = a.cu_seqlens[lo + 1];
+      if (c0 <= tok && tok < c1) {
+        s_seq = lo;
+        s_pos = static_cast<long long>(a.pos_start[lo]) + (tok - c0);
+      }
     }
   }
   xs[j] = xv;
   __syncthreads();
   if (j >= ud.r) return;
   // token -> page: the block-table entry is loaded before the arithmetic below
-  const int s = s_seq;
-  const long long pos = s_pos;
-  const bool pos_ok = pos >= 0 && pos < static_cast<long long>(a.max_pages) * kPage;
-  const int lp = pos_ok ? static_cast<int>(pos / kPage) : 0;
-  const int slot = pos_ok ? static_cast<int>(pos % kPage) : 0;
-  const int32_t pid = pos_ok ? a.block_table[static_cast<size_t>(s) * a.max_pages + lp] : -1;
+  bool pos_ok = true;
+  int slot = static_cast<int>(place % kPage);
+  long long pid = place / kPage;
+  if constexpr (!kSlots) {
+    const int s = s_seq;
+    const long long pos = s_pos;
+    pos_ok = pos >= 0 && pos < static_cast<long long>(a.max_pages) * kPage;
+    const int lp = pos_ok ? static_cast<int>(pos / kPage) : 0;
+    slot = pos_ok ? static_cast<int>(pos % kPage) : 0;
+    pid = pos_ok ? a.block_table[static_cast<size_t>(s) * a.max_pages + lp] : -1;
+  }
 
   uint32_t code = 0;
   if (raw) {
@@ -247,19 +259,11 @@ extern "C" kvtc_status kvtc_debug_encode_latent(const kvtc_plan* plan, int layer
   return KVTC_OK;
 }
 
-extern "C" kvtc_status kvtc_encode_append(const kvtc_plan* plan, const kvtc_cache* cache, int layer,
-                                          const void* k, const void* v, kvtc_dtype dtype,
-                                          const int32_t* cu_seqlens, const int32_t* pos_start, int n_tok,
-                                          void* stream) {
-  kvtc_status st = check_uploaded(plan);
-  if (st != KVTC_OK) return st;
-  if (!cache || !cache->pool || !cache->block_table) return fail(KVTC_EINVAL, "cache is incomplete");
-  if (layer < 0 || layer >= plan->L) return fail(KVTC_EINVAL, "layer out of range");
-  if (dtype != KVTC_F32 && dtype != KVTC_BF16) return fail(KVTC_EINVAL, "dtype must be F32 or BF16");
-  if (n_tok < 0 || cache->n_seq < 1 || cache->max_pages < 1) return fail(KVTC_EINVAL, "bad sizes");
-  if (n_tok == 0) return KVTC_OK;
-  if (!k || !v || !cu_seqlens || !pos_start) return fail(KVTC_EINVAL, "null device pointer");
-  if (reinterpret_cast<uintptr_t>(cache->pool) & 15) return fail(KVTC_EINVAL, "pool must be 16-byte aligned");
+namespace {
+
+kvtc_status launch_append(const kvtc_plan* plan, const kvtc_cache* cache, int layer, const void* k, const void* v,
+                          kvtc_dtype dtype, const int32_t* cu_seqlens, const int32_t* pos_start,
+                          const int64_t* slot_map, int n_tok, void* stream) {
   AppendArgs a;
   a.units = plan->d_units;
   a.unit0 = layer * plan->H * 2;
@@ -276,6 +280,7 @@ extern "C" kvtc_status kvtc_encode_append(const kvtc_plan* plan, const kvtc_cach
   a.pages_per_unit = cache->pages_per_unit;
   a.block_table = cache->block_table;
   a.max_pages = cache->max_pages;
+  a.slots = slot_map;
   a.status = cache->status;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_tok), static_cast<unsigned>(a.n_units));
@@ -286,8 +291,43 @@ extern "C" kvtc_status kvtc_encode_append(const kvtc_plan* plan, const kvtc_cach
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, encode_append_kernel, a);
+  cudaError_t e = slot_map ? cudaLaunchKernelEx(&cfg, encode_append_kernel<true>, a)
+                           : cudaLaunchKernelEx(&cfg, encode_append_kernel<false>, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "encode_append launch");
   return KVTC_OK;
+}
+
+}  // namespace
+
+extern "C" kvtc_status kvtc_encode_append(const kvtc_plan* plan, const kvtc_cache* cache, int layer,
+                                          const void* k, const void* v, kvtc_dtype dtype,
+                                          const int32_t* cu_seqlens, const int32_t* pos_start, int n_tok,
+                                          void* stream) {
+  kvtc_status st = check_uploaded(plan);
+  if (st != KVTC_OK) return st;
+  if (!cache || !cache->pool || !cache->block_table) return fail(KVTC_EINVAL, "cache is incomplete");
+  if (layer < 0 || layer >= plan->L) return fail(KVTC_EINVAL, "layer out of range");
+  if (dtype != KVTC_F32 && dtype != KVTC_BF16) return fail(KVTC_EINVAL, "dtype must be F32 or BF16");
+  if (n_tok < 0 || cache->n_seq < 1 || cache->max_pages < 1) return fail(KVTC_EINVAL, "bad sizes");
+  if (n_tok == 0) return KVTC_OK;
+  if (!k || !v || !cu_seqlens || !pos_start) return fail(KVTC_EINVAL, "null device pointer");
+  if (reinterpret_cast<uintptr_t>(cache->pool) & 15) return fail(KVTC_EINVAL, "pool must be 16-byte aligned");
+  return launch_append(plan, cache, layer, k, v, dtype, cu_seqlens, pos_start, nullptr, n_tok, stream);
+}
+
+extern "C" kvtc_status kvtc_encode_append_slots(const kvtc_plan* plan, const kvtc_cache* cache, int layer,
+                                                const void* k, const void* v, kvtc_dtype dtype,
+                                                const int64_t* slot_map, int n_tok, void* stream) {
+  kvtc_status st = check_uploaded(plan);
+  if (st != KVTC_OK) return st;
+  if (!cache || !cache->pool) return fail(KVTC_EINVAL, "cache is incomplete");
+  if (layer < 0 || layer >= plan->L) return fail(KVTC_EINVAL, "layer out of range");
+  if (dtype != KVTC_F32 && dtype != KVTC_BF16) return fail(KVTC_EINVAL, "dtype must be F32 or BF16");
+  if (n_tok < 0) return fail(KVTC_EINVAL, "n_tok must be >= 0");
+  if (n_tok == 0) return KVTC_OK;
+  if (!k || !v || !slot_map) return fail(KVTC_EINVAL, "null device pointer");
+  if (reinterpret_cast<uintptr_t>(slot_map) & 7) return fail(KVTC_EINVAL, "slot_map must be 8-byte aligned");
+  if (reinterpret_cast<uintptr_t>(cache->pool) & 15) return fail(KVTC_EINVAL, "pool must be 16-byte aligned");
+  return launch_append(plan, cache, layer, k, v, dtype, nullptr, nullptr, slot_map, n_tok, stream);
 }

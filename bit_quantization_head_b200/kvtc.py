@@ -96,6 +96,7 @@ def lib():
         "kvtc_cache_bytes": (C.c_uint64, [_P, C.c_uint64]),
         "kvtc_unit_pool_offset": (C.c_uint64, [_P, C.c_int, C.c_uint64]),
         "kvtc_encode_append": (st, [_P, C.POINTER(CacheDesc), C.c_int, _P, _P, C.c_int, _P, _P, C.c_int, _P]),
+        "kvtc_encode_append_slots": (st, [_P, C.POINTER(CacheDesc), C.c_int, _P, _P, C.c_int, _P, C.c_int, _P]),
         "kvtc_encode_prefill": (st, [_P, C.POINTER(CacheDesc), C.c_int, _P, _P, C.c_int, C.c_int, C.c_int, _P]),
         "kvtc_plan_prefill_stats": (st, [_P, C.POINTER(C.c_uint64), C.POINTER(C.c_uint64), C.c_int]),
         "kvtc_debug_encode_latent": (st, [_P, C.c_int, C.c_int, C.c_int, _P, C.c_int, C.c_int, _P, _P]),
@@ -304,6 +305,18 @@ def kvtc_encode_append(plan, cache, layer, k, v, cu_seqlens, pos_start, stream=N
     _check(lib().kvtc_encode_append(plan.handle, C.byref(cache.desc), layer, _dev_ptr(k), _dev_ptr(v),
                                     _dtype_code(k), _dev_ptr(cu_seqlens), _dev_ptr(pos_start), k.shape[0],
                                     _stream(stream)))
+
+
+def kvtc_encode_append_slots(plan, cache, layer, k, v, slot_map, stream=None):
+    """kvtc_encode_append with the place of every row given (int64 [n_tok], as kvtc_step_tables
+    makes it; negative: skipped)."""
+    import torch
+    if slot_map.dtype != torch.int64 or slot_map.numel() != k.shape[0]:
+        raise ValueError(f"slot_map must be int64 with {k.shape[0]} elements")
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("k and v must have the same shape and dtype")
+    _check(lib().kvtc_encode_append_slots(plan.handle, C.byref(cache.desc), layer, _dev_ptr(k), _dev_ptr(v),
+                                          _dtype_code(k), _dev_ptr(slot_map), k.shape[0], _stream(stream)))
 
 
 def kvtc_encode_prefill(plan, cache, layer, k, v, seq, pos_start, stream=None):

@@ -251,6 +251,18 @@ kvtc_status kvtc_encode_append(const kvtc_plan* plan, const kvtc_cache* cache, i
                                void* stream);
 
 /*
+ * kvtc_encode_append_slots -- kvtc_encode_append with the place of every row given, as
+ * kvtc_step_tables makes it: slot_map, device int64 [n_tok], page id * 128 + token of the
+ * page.  A negative slot is skipped (a padding row, or one of a sequence that got no page); one
+ * beyond pages_per_unit * 128 is skipped and sets KVTC_STATUS_BAD_PAGE.  Neither the block
+ * table nor its sizes are read (it may be NULL).  Codes, types and races otherwise as
+ * kvtc_encode_append.
+ */
+kvtc_status kvtc_encode_append_slots(const kvtc_plan* plan, const kvtc_cache* cache, int layer,
+                                     const void* k, const void* v, kvtc_dtype dtype,
+                                     const int64_t* slot_map, int n_tok, void* stream);
+
+/*
  * kvtc_encode_prefill -- the same codes as kvtc_encode_append for one sequence's
  * page-aligned span, computed as 128-token x d by d x r_u tensor-core GEMM tiles
  * (tcgen05, TMEM accumulators) whose epilogue quantizes and packs whole pages.  Any
@@ -377,16 +389,20 @@ kvtc_status kvtc_decode_attention_noalloc(const kvtc_plan* plan, const kvtc_cach
  * kvtc_step_tables -- the tables of one serving step, built on the GPU from the request
  * lengths: block table growth from a ring of free pages, the pages of finished requests
  * back into it, and the row layout of the step's new tokens.  No counterpart on the
- * KV-COBRA pages (paging as in PagedAttention); its outputs are what kvtc_encode_append
- * (cu_seqlens; pos_start = cached_lens), kvtc_raw_append (slot_map, positions) and the
- * decode calls (block table, seq_lens) read.
+ * KV-COBRA pages (paging as in PagedAttention); its outputs are what
+ * kvtc_encode_append_slots and kvtc_raw_append (slot_map, positions),
+ * kvtc_raw_cross_attention (cu_seqlens) and the decode calls (block table, seq_lens) read.
+ * kvtc_encode_append and kvtc_encode_prefill write through the block table, wherever a row of
+ * it points: they may take these tables (cu_seqlens; pos_start = cached_lens) only once status
+ * is known to be clear, since a sequence that could not take its tokens keeps its rows in
+ * cu_seqlens while its table row may still name pages that have gone to others.
  *
  * Sequence s holds c = cached_lens[s] tokens, in pages block_table[s][0 .. ceil(c/128)),
  * and brings n = new_lens[s] new ones (n < 0: the sequence has finished).  In sequence
  * order:
  *   finished: its ceil(c/128) page ids are appended to the ring's tail; seq_lens[s] = 0.
- *     Its block table row is left as it is.  Pages given back become available from the
- *     next call on.
+ *     Its block table row is left as it is (entries behind seq_lens[s] name no page of the
+ *     sequence).  Pages given back become available from the next call on.
  *   otherwise: its rows are cu_seqlens[s] .. cu_seqlens[s] + n - 1; the
  *     need = ceil((c+n)/128) - ceil(c/128) pages that it lacks are taken from the ring's
  *     head and entered in its block table row; seq_lens[s] = c + n; row i of it gets
