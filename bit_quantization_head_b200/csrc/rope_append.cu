@@ -310,8 +310,8 @@ extern "C" kvtc_status kvtc_raw_append(const kvtc_raw_cache* cache, int layer, c
     if (st != KVTC_OK) return st;
   }
   if (q && !rope) return fail(KVTC_EINVAL, "q is rotated: it needs a rope description");
+  if (n_tok == 0) return KVTC_OK;  // (empty tensors have null pointers)
   if (!q && n_q_heads != 0) return fail(KVTC_EINVAL, "null device pointer");
-  if (n_tok == 0) return KVTC_OK;
   if (!slot_map || (rope && !positions) || (q && !q_out)) return fail(KVTC_EINVAL, "null device pointer");
   st = check_rows(k, k_stride, cache->n_kv_heads, 2, nullptr);
   if (st == KVTC_OK) st = check_rows(v, v_stride, cache->n_kv_heads, 2, nullptr);
