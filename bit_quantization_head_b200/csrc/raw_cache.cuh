@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <utility>
 
 #include "kvtc_internal.h"
@@ -61,9 +62,29 @@ inline uint64_t pool_bytes(const kvtc_raw_cache* c) {
   return static_cast<uint64_t>(c->n_layers) * c->n_pages * static_cast<uint64_t>(c->n_kv_heads) * 2 * kKindElems * 2;
 }
 
-// What an attention call writes shares memory with nothing else that it touches.
+struct Range {
+  const void* p;
+  uint64_t bytes;
+};
+inline bool overlaps_any(const void* p, uint64_t bytes, std::initializer_list<Range> others) {
+  for (const Range& r : others)
+    if (overlap(p, bytes, r.p, r.bytes)) return true;
+  return false;
+}
+
+// What an attention call writes shares memory with nothing else that it touches (cu_q: null
+// without query offsets).
 inline kvtc_status check_overlap(const kvtc_raw_cache* c, const void* q, const void* out, uint64_t rows, const void* ws,
-                                 uint64_t ws_bytes) {
+                                 uint64_t ws_bytes, const int32_t* seq_lens, const int32_t* cu_q) {
+  const uint64_t n = static_cast<uint64_t>(c->n_seq);
+  const std::initializer_list<Range> lists = {{seq_lens, 4 * n},
+                                              {cu_q, 4 * (n + 1)},
+                                              {c->block_table, 4 * n * static_cast<uint64_t>(c->max_pages)}};
+  if (overlaps_any(out, rows, lists) || overlaps_any(ws, ws_bytes, lists))
+    return fail(KVTC_EINVAL, "out or the workspace overlaps the lengths, the row offsets or the block table");
+  if (overlaps_any(c->status, 4, lists) ||
+      overlaps_any(c->status, 4, {{out, rows}, {ws, ws_bytes}, {q, rows}, {c->pool, pool_bytes(c)}}))
+    return fail(KVTC_EINVAL, "the status word overlaps another buffer");
   if (overlap(q, rows, out, rows)) return fail(KVTC_EINVAL, "out overlaps q");
   if (overlap(out, rows, c->pool, pool_bytes(c)) || overlap(out, rows, ws, ws_bytes))
     return fail(KVTC_EINVAL, "out overlaps the pool or the workspace");

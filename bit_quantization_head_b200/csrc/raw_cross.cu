@@ -1036,7 +1036,8 @@ extern "C" kvtc_status kvtc_raw_cross_attention(const kvtc_raw_cache* cache, int
   if (workspace_bytes < kvtc_raw_cross_workspace_bytes(cache->n_seq, n_tok, n_q_heads, cache->n_kv_heads, max_seq_len))
     return fail(KVTC_ECAPACITY, "cross attention workspace too small");
   st = raw::check_overlap(cache, q, out, static_cast<uint64_t>(n_tok) * n_q_heads * kD * 2, workspace,
-                          kvtc_raw_cross_workspace_bytes(cache->n_seq, n_tok, n_q_heads, cache->n_kv_heads, max_seq_len));
+                          kvtc_raw_cross_workspace_bytes(cache->n_seq, n_tok, n_q_heads, cache->n_kv_heads, max_seq_len),
+                          seq_lens, cu_q);
   if (st != KVTC_OK) return st;
   int sms = 0;
   st = raw::sm_count(&sms);

@@ -677,7 +677,8 @@ extern "C" kvtc_status kvtc_raw_decode_attention(const kvtc_raw_cache* cache, in
   if (workspace_bytes < kvtc_raw_decode_workspace_bytes(cache->n_seq, n_q_heads, cache->n_kv_heads, max_seq_len))
     return fail(KVTC_ECAPACITY, "decode workspace too small");
   st = raw::check_overlap(cache, q, out, static_cast<uint64_t>(cache->n_seq) * n_q_heads * kD * 2, workspace,
-                          kvtc_raw_decode_workspace_bytes(cache->n_seq, n_q_heads, cache->n_kv_heads, max_seq_len));
+                          kvtc_raw_decode_workspace_bytes(cache->n_seq, n_q_heads, cache->n_kv_heads, max_seq_len),
+                          seq_lens, nullptr);
   if (st != KVTC_OK) return st;
   int sms = 0;
   st = raw::sm_count(&sms);

@@ -204,9 +204,9 @@ kvtc_status check_rows(const void* x, int64_t stride, int heads, size_t es, cons
   return KVTC_OK;
 }
 
-// No output may share memory with an input or the other output, but for rows rotated in
-// place (the same contiguous rows).
-kvtc_status check_rope_overlap(const RopeArgs& a, size_t es, const kvtc_raw_cache* cache) {
+// No output may share memory with an input, with the positions (of n_axes axes) and slots, or
+// with the other output, but for rows rotated in place (the same contiguous rows).
+kvtc_status check_rope_overlap(const RopeArgs& a, size_t es, int n_axes, const kvtc_raw_cache* cache) {
   const void* out[2] = {a.q_out, a.k_out};
   uint64_t span[3], dense[3];
   for (int i = 0; i < 3; ++i) {
@@ -221,7 +221,17 @@ kvtc_status check_rope_overlap(const RopeArgs& a, size_t es, const kvtc_raw_cach
     }
   }
   if (raw::overlap(out[0], dense[0], out[1], dense[1])) return fail(KVTC_EINVAL, "the outputs overlap");
+  const uint64_t n = static_cast<uint64_t>(a.n_tok);
+  const std::initializer_list<raw::Range> lists = {{a.positions, 4 * n * static_cast<uint64_t>(n_axes)}, {a.slots, 8 * n}};
+  if (raw::overlaps_any(out[0], dense[0], lists) || raw::overlaps_any(out[1], dense[1], lists))
+    return fail(KVTC_EINVAL, "an output overlaps the positions or the slots");
   if (cache) {
+    if (raw::overlaps_any(cache->pool, raw::pool_bytes(cache), lists))
+      return fail(KVTC_EINVAL, "the positions or the slots overlap the pool");
+    if (raw::overlaps_any(cache->status, 4, lists) ||
+        raw::overlaps_any(cache->status, 4, {{cache->pool, raw::pool_bytes(cache)}, {out[0], dense[0]},
+                                             {a.x[0], span[0]}, {a.x[1], span[1]}, {a.x[2], span[2]}}))
+      return fail(KVTC_EINVAL, "the status word overlaps another buffer");
     bool pool = raw::overlap(out[0], dense[0], cache->pool, raw::pool_bytes(cache));
     for (int i = 0; i < 3; ++i) pool |= raw::overlap(a.x[i], span[i], cache->pool, raw::pool_bytes(cache));
     if (pool) return fail(KVTC_EINVAL, "rows overlap the pool");
@@ -287,7 +297,7 @@ extern "C" kvtc_status kvtc_rope(const kvtc_rope_desc* rope, const void* q, int6
   a.k_out = k_out;
   a.positions = positions;
   a.n_tok = n_tok;
-  st = check_rope_overlap(a, es, nullptr);
+  st = check_rope_overlap(a, es, rope->n_axes, nullptr);
   if (st != KVTC_OK) return st;
   return launch_rope(a, dtype, stream);
 }
@@ -334,7 +344,7 @@ extern "C" kvtc_status kvtc_raw_append(const kvtc_raw_cache* cache, int layer, c
   a.positions = positions;
   a.n_tok = n_tok;
   a.status = cache->status;
-  st = check_rope_overlap(a, 2, cache);
+  st = check_rope_overlap(a, 2, rope ? rope->n_axes : 0, cache);
   if (st != KVTC_OK) return st;
   return launch_rope(a, cache->dtype, stream);
 }

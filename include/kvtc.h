@@ -456,8 +456,9 @@ typedef struct {
  * or F16); k likewise.  q or k may be NULL (with 0 heads).  positions: device int32
  * [n_axes][n_tok] (any int32; a negative position rotates backwards).  q_out, k_out:
  * device [n_tok][heads][128], contiguous; q_out may be q where q_stride = n_q_heads * 128
- * (k likewise), no other overlap.  All row pointers 16-byte aligned, strides multiples of
- * 16 bytes and at least heads * 128.  At most 1024 heads each.
+ * (k likewise); the outputs share memory with nothing else of the call.  All row pointers
+ * 16-byte aligned, strides multiples of 16 bytes and at least heads * 128.  At most 1024
+ * heads each.
  */
 kvtc_status kvtc_rope(const kvtc_rope_desc* rope, const void* q, int64_t q_stride, int n_q_heads, const void* k,
                       int64_t k_stride, int n_kv_heads, kvtc_dtype dtype, const int32_t* positions, int n_tok,
@@ -497,8 +498,8 @@ uint64_t kvtc_raw_cache_bytes(int n_layers, uint64_t n_pages, int n_kv_heads);
  * attention.  k, v: row t of head h at k + t * k_stride + h * 128, of the cache's dtype.
  * slot_map: device int64 [n_tok]: a negative slot is skipped (a padding row; q is rotated
  * all the same), one beyond n_pages * 128 is skipped and sets KVTC_STATUS_BAD_PAGE.  Rows
- * that name the same slot race.  positions, q, q_out, strides and alignment as kvtc_rope; no
- * rows in or out may lie in the pool.
+ * that name the same slot race.  positions, q, q_out, strides and alignment as kvtc_rope;
+ * nothing else of the call may lie in the pool, and the status word in no other buffer.
  * The block table is not read (it may be NULL).
  */
 kvtc_status kvtc_raw_append(const kvtc_raw_cache* cache, int layer, const void* k, int64_t k_stride, const void* v,
@@ -515,10 +516,11 @@ uint64_t kvtc_raw_cross_workspace_bytes(int n_seq, int n_tok, int n_q_heads, int
  * pages: o = sum_t p_t v_t, p = softmax over t < seq_lens[s] of softmax_scale * q . k_t
  * (0 means 1/sqrt(128)), fp32 accumulation and statistics.  Query head g of KV head h is
  * q head h * (n_q_heads / n_kv_heads) + g, as in kvtc_decode_attention.
- * q, out: device [n_seq][n_q_heads][128] of the cache's dtype, 16-byte aligned; out, q, the
- * pool and the workspace may not overlap.  seq_lens: device int32 [n_seq]; 0 gives an all-zero output; a length
- * outside [0, max_seq_len] sets KVTC_STATUS_BAD_POS, and a page id outside the pool among
- * the pages read KVTC_STATUS_BAD_PAGE: the outputs of that sequence's heads are then zero.
+ * q, out: device [n_seq][n_q_heads][128] of the cache's dtype, 16-byte aligned.  What the call
+ * writes (out, workspace, status word) may share memory with nothing else of it.
+ * seq_lens: device int32 [n_seq]; 0 gives an all-zero output; a length outside
+ * [0, max_seq_len] sets KVTC_STATUS_BAD_POS, and a page id outside the pool among the pages
+ * read KVTC_STATUS_BAD_PAGE: the outputs of that sequence's heads are then zero.
  * max_seq_len: host bound, at most max_pages * 128.  workspace: device, 16-byte aligned,
  * at least kvtc_raw_decode_workspace_bytes, zero-filled before its first use; every call
  * leaves its counters at zero again, so one workspace serves any number of consecutive
