@@ -42,6 +42,11 @@ inline kvtc_status check_cache(const kvtc_raw_cache* c, int layer) {
   return KVTC_OK;
 }
 
+// The factor from a score to the exponent of 2 of its weight (scale 0 means 1 / sqrt(128)).
+inline float exp2_scale(float scale) {
+  return (scale > 0.0f ? scale : 1.0f / std::sqrt(static_cast<float>(kD))) * 1.4426950408889634f;
+}
+
 // What both attention calls need beyond that.
 inline kvtc_status check_attention(const kvtc_raw_cache* c, int layer, int n_q_heads, int max_group, int max_seq_len,
                                    float scale) {
@@ -55,6 +60,7 @@ inline kvtc_status check_attention(const kvtc_raw_cache* c, int layer, int n_q_h
   if (max_seq_len < 0 || max_seq_len > static_cast<long long>(c->max_pages) * kPage)
     return fail(KVTC_EINVAL, "max_seq_len exceeds the block table");
   if (!std::isfinite(scale) || scale < 0.0f) return fail(KVTC_EINVAL, "softmax_scale must be finite and >= 0");
+  if (!std::isfinite(exp2_scale(scale))) return fail(KVTC_EINVAL, "softmax_scale is too large");
   return KVTC_OK;
 }
 

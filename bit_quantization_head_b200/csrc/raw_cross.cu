@@ -1056,7 +1056,7 @@ extern "C" kvtc_status kvtc_raw_cross_attention(const kvtc_raw_cache* cache, int
   a.tile_tok = raw::kRows / a.G;
   a.row0 = static_cast<int>(static_cast<uint64_t>(layer) * cache->n_pages * static_cast<uint64_t>(a.H) * 2 * kPage);
   a.out = static_cast<uint16_t*>(out);
-  a.c = (softmax_scale > 0.0f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(kD))) * 1.4426950408889634f;
+  a.c = raw::exp2_scale(softmax_scale);
   a.tickets = static_cast<int*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + 4096);
   a.status = cache->status;

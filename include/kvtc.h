@@ -514,7 +514,8 @@ uint64_t kvtc_raw_cross_workspace_bytes(int n_seq, int n_tok, int n_q_heads, int
 /*
  * kvtc_raw_decode_attention -- one new token per sequence over one layer's uncompressed
  * pages: o = sum_t p_t v_t, p = softmax over t < seq_lens[s] of softmax_scale * q . k_t
- * (0 means 1/sqrt(128)), fp32 accumulation and statistics.  Query head g of KV head h is
+ * (>= 0 and up to 2.3e38, where it still fits fp32 in powers of two; 0 means 1/sqrt(128)),
+ * fp32 accumulation and statistics.  Query head g of KV head h is
  * q head h * (n_q_heads / n_kv_heads) + g, as in kvtc_decode_attention.
  * q, out: device [n_seq][n_q_heads][128] of the cache's dtype, 16-byte aligned.  What the call
  * writes (out, workspace, status word) may share memory with nothing else of it.
