@@ -57,7 +57,10 @@ def _compile(src, verbose):
 
 def _build_marshal():
     """The binding's compiled half (csrc/marshal.cpp): a CPython module against torch."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    torch_dir = spec.submodule_search_locations[0]
     src = os.path.join(CSRC, "marshal.cpp")
     h = hashlib.sha256()
     for path in (src, os.path.join(ROOT, "include", "kvtc.h"), os.path.join(torch_dir, "version.py")):
@@ -86,7 +89,7 @@ def build(verbose=False):
     with cf.ThreadPoolExecutor(max_workers=max(2, os.cpu_count() or 2)) as ex:
         marshal = ex.submit(_build_marshal)
         results = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        marshal.result()
+        marshal_error = marshal.exception()
     objs = [r[0] for r in results]
     if verbose:
         for (o, log), s in zip(results, SOURCES):
@@ -98,6 +101,13 @@ def build(verbose=False):
     if p.returncode != 0:
         raise RuntimeError(f"link failed\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, LIB)
+    if marshal_error is not None:
+        # The library stands without it (a user of the C interface needs neither torch's headers
+        # nor Python's); one of an earlier build must not be bound to this library.
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        raise RuntimeError("libkvtc.so is built, the binding's compiled half (kvtc_step_tables and the calls "
+                           f"after it in kvtc.py) is not: {marshal_error}") from marshal_error
     return LIB
 
 
