@@ -41,10 +41,10 @@ template <typename T>
 constexpr int kBatchOf = sizeof(T) == 4 ? 2 : 4;
 template <typename T>
 constexpr int kBlocksOf = sizeof(T) == 4 ? 4 : 3;
-// Warps from which a token has no more than one: every further warp of a token makes its
-// sines again (2000 tokens of 40 heads 9.8 us with 12 or less per SM, 10.0 with 24, 12.8 with
-// 48; 300 tokens 4.6 with 12, 5.5 with 24).
-constexpr int kBusyWarps = 148 * 12;
+// Warps per SM from which a token has no more than one: every further warp of a token makes
+// its sines again (2000 tokens of 40 heads 9.8 us with 12 or less, 10.0 with 24, 12.8 with 48;
+// 300 tokens 4.6 with 12, 5.5 with 24).
+constexpr int kBusyWarpsPerSm = 12;
 
 struct RopeArgs {
   const void* x[3];        // q, k, v (null: absent)
@@ -244,7 +244,11 @@ kvtc_status launch_rope(RopeArgs& a, kvtc_dtype dtype, void* stream) {
   const int at_once = dtype == KVTC_F32 ? 2 : 4;  // rows a warp moves at a time
   const int n_all = a.heads[0] + a.heads[1] + a.heads[2];
   const int most = (n_all + at_once - 1) / at_once;
-  const int want = std::min(most, (kBusyWarps + a.n_tok - 1) / a.n_tok);
+  int sms = 0;
+  const kvtc_status st = raw::sm_count(&sms);
+  if (st != KVTC_OK) return st;
+  const long long busy = static_cast<long long>(kBusyWarpsPerSm) * sms;
+  const int want = static_cast<int>(std::min<long long>(most, (busy + a.n_tok - 1) / a.n_tok));
   a.part_rows = (most + want - 1) / want * at_once;
   a.parts = (n_all + a.part_rows - 1) / a.part_rows;
   const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.n_tok) * a.parts + kWarps - 1) / kWarps);
