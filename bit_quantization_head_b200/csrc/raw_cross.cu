@@ -12,7 +12,10 @@
 // under the power cap (1.13 PFLOP/s; a plain matrix product holds 1.40 there).  A step of two
 // tiles takes about 3000 cycles, 2048 of them of the tensor pipe: the row warps issue about
 // 1850 instructions for it on each scheduler, many of them double-width, beside 1280 cycles
-// of exponentials.
+// of exponentials.  Smaller calls (two tiles a unit, one unit per CTA, pages in L2): 11 us and
+// 1.65 us a step; every further unit of a CTA 7 us for its start and output beside its steps.
+// Times here and below are of calls replayed from a graph on the same inputs; with inputs that
+// change, calls of tens of us take 3 to 6 us more.
 //
 // Rows of a tile: the tokens' query heads of one KV head (token-major, as many whole tokens
 // as fit in 128 rows), so K and V are read once for all of them.  A unit is (sequence, KV
@@ -62,7 +65,10 @@ constexpr int kRowRegs = 208, kOtherRegs = 88;
 // (a ragged batch of 8 with units of 1 and of 12 steps: 73 us with 0, 52 with 1 to 3; 16
 // sequences of 40 tokens over 500 states 27.6, 26.4 with 1, 25.5 with 2, 22.6 with 3).
 constexpr int kUnitCost = 3;
-// Steps of a unit of one tile from which the second tile takes every other one.
+// Steps of a unit of one tile from which the second tile takes every other one (16 answers of
+// one token and 20 heads over 500 states, 4 steps: 27.5 us, 29.3 without; 200 of 20 tokens over
+// 400 states 95 and 102; over 1500 states 52 and 54.  From 2 steps on instead: no difference
+// beyond 1.5 us either way).
 constexpr int kTwinSteps = 4;
 // Pairs of eight whose weights are formed on the FMA pipe: three balance it against the
 // exponential unit (4 x 1500 states of 20 heads: none 43.0 us, 1 41.5, 2 40.4, 3 39.9, 4 41.5).

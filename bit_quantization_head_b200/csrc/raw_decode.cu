@@ -5,17 +5,24 @@
 // share each K and V tile.
 //
 // Bound: HBM, 512 bytes per token and KV head for 4 * 128 flops per query head; the arithmetic
-// runs as m16n8k16 MMAs (scores: 16 tokens x 8 heads; values: 16 dims x 8 heads).  Measured:
-// 16 x 32768 tokens of 8 KV heads in 331 us (6.5 TB/s, the rate of a copy), one sequence of
-// 131072 tokens and 4 KV heads in 56 us (41 at that rate: about 4 us until the first tiles
-// are there, 6 to join 74 parts of a head), 4096 tokens in 10.8 us and three chats of up to
-// 1000 tokens in 8.6 us (launch, two dependent reads, a tile, and the join of its parts).
+// runs as m16n8k16 MMAs (scores: 16 tokens x 8 heads; values: 16 dims x 8 heads).  Measured
+// with up to 8 query heads per KV head: 16 x 32768 tokens of 8 KV heads in 330 us (6.5 TB/s,
+// the rate of a copy), one sequence of 131072 tokens and 4 KV heads in 55 us (41 at that rate:
+// about 4 us until the first tiles are there, 6 to join 74 parts of a head), 4096 tokens in
+// 10.4 us and three chats of up to 1000 tokens in 8.6 us (launch, two dependent reads, a tile,
+// and the join of its parts).  With 9 to 16 query heads the consumers are the bound: 446 us for
+// the same 16 x 32768 tokens (12 or 16 heads; 4.8 TB/s), 15.6 us for the three chats, 71 us for
+// 131072 tokens of 4 KV heads; above 16 heads K and V are read again for every further 16 (17
+// or 32 heads 883 us).
 //
-// Work split.  A unit is (sequence, KV head, group of query heads), its tiles 64 tokens.  All
-// tiles of all units in a row are cut into one equal run per CTA (2 CTAs per SM), whatever
-// the lengths are, found on the device from seq_lens: a ragged batch and a single long
-// sequence load every SM alike, and the workspace does not grow with the batch (one CTA per
-// SM with twice the ring: 440 us for 16 x 32768, its four warps do not keep up).  A run
+// Work split.  A unit is (sequence, KV head, group of up to 8 or 16 query heads), its tiles 64
+// tokens.  All tiles of all units in a row are cut into one equal run per CTA, whatever the
+// lengths are, found on the device from seq_lens: a ragged batch and a single long sequence
+// load every SM alike, and the workspace does not grow with the batch.  Up to 8 heads: two CTAs
+// per SM with rings of three tiles (one with twice the ring: 440 us for 16 x 32768, its four
+// warps do not keep up).  9 to 16: one CTA per SM with a ring of five (two rings of three do not
+// fit in shared memory while every stage has room for the queries; neither that nor more
+// consumer warps were tried).  A run
 // covers whole units but for its first and last; those leave a partial (m, l, z) and the
 // last CTA of the unit to arrive (a counter kept by the unit's first CTA) joins them in
 // order, so results do not depend on timing.
@@ -340,6 +347,9 @@ __device__ __forceinline__ bool join_parts(const DecodeArgs& a, Smem<NT>& s, int
 // The same in two levels: groups of CTAs, then the groups' parts.
 template <int NT, bool F16>
 __device__ __noinline__ bool join_groups(const DecodeArgs& a, Smem<NT>& s, int c0, int shares, int heads, size_t out0) {
+  // Groups of 8 up to 128 parts, of 16 above (74 parts of 7 heads over 131072 tokens 54.3 us
+  // with 8, 56.8 with 16; 128 parts of 8 heads 17.9 and 19.1; 148 parts of 4 heads 33.1 and
+  // 33.8; 296 parts of 8 heads 26.1 and 24.7).
   const int group = shares <= 128 ? 8 : 16;
   const int begin = (static_cast<int>(blockIdx.x) - c0) / group * group, first = c0 + begin;
   if (!join_parts<NT, F16, false>(a, s, a.tickets + 2 * first + (begin == 0), c0, first, 1, min(group, shares - begin),
@@ -553,8 +563,8 @@ __device__ void consume(const DecodeArgs& a, Smem<NT>& s) {
       continue;
     }
     // ---- the unit is shared with other CTAs: the last one to arrive joins the partials; of
-    // many, groups of CTAs first (74 parts read one after another took 13 us at the end of a
-    // call; groups are joined while other CTAs still compute, and cost 2 us of their own)
+    // many, groups of CTAs first (joined while other CTAs still compute; at once, 74 parts
+    // took 59.8 us instead of 54.3, 296 of 8 heads 49 instead of 25)
     const int shares = d.c1 - d.c0 + 1;
     bool ok;
     if (shares <= 48)

@@ -13,9 +13,11 @@
 // registers.  The token's 64 are made once, two (cos, sin) per lane, and dealt through the
 // warp's shared memory, after the loads of the first rows have been issued; warps never wait
 // for one another (a block of a few tokens that shared them behind a barrier reached 3.3 TB/s,
-// at two blocks per SM).  Few tokens: a token's rows are dealt over several warps.  Measured:
-// 32768 bf16 tokens of 40 heads in 102 us (6.6 TB/s, the rate of a copy), 16411 tokens into
-// pages in 64.5 us (6.3 TB/s), 4097 fp32 tokens of 32 heads in 20.9 us, 16 tokens in 3.2 us.
+// at two blocks per SM).  Few tokens: a token's rows are dealt over several warps.  Measured on
+// inputs that change from call to call: 32768 bf16 tokens of 40 heads in 105 us (6.4 TB/s, the
+// rate of a copy), 16411 tokens into pages in 66 us (6.1 TB/s), 4097 fp32 tokens of 32 heads in
+// 26 us (5.2 TB/s; replayed on the same rows, half of them still in L2, 20.9), 16 tokens in
+// 3.9 us (3.2 replayed).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,9 +36,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kHalf = kD / 2;
-// Rows of a lane in flight, and blocks per SM: 4 and 3 in 16 bits (32768 tokens 102.5 us, 104.3
-// with 2 and 4), 2 and 4 in fp32 (4097 tokens of 32 heads, two warps a token: 21.6 us, 23.9
-// with 4 and 3).
+// Rows of a lane in flight, and blocks per SM, replayed on the same rows: 4 and 3 in 16 bits
+// (32768 tokens 102.5 us, 104.3 with 2 and 4), 2 and 4 in fp32 (4097 tokens of 32 heads, with two
+// warps a token: 21.6 us, 23.9 with 4 and 3; one warp a token, as they have now, 20.9).
 template <typename T>
 constexpr int kBatchOf = sizeof(T) == 4 ? 2 : 4;
 template <typename T>
