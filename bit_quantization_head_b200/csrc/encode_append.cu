@@ -10,6 +10,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "kvtc_internal.h"
 #include "layout.cuh"
 #include "ptx.cuh"
@@ -128,17 +130,17 @@ __global__ void __launch_bounds__(128) encode_append_kernel(const __grid_constan
   __syncthreads();
   if (j >= ud.r) return;
   // token -> page: the block-table entry is loaded before the arithmetic below
-  bool pos_ok = true;
-  int slot = static_cast<int>(place % kPage);
-  long long pid = place / kPage;
-  if constexpr (!kSlots) {
-    const int s = s_seq;
-    const long long pos = s_pos;
-    pos_ok = pos >= 0 && pos < static_cast<long long>(a.max_pages) * kPage;
-    const int lp = pos_ok ? static_cast<int>(pos / kPage) : 0;
-    slot = pos_ok ? static_cast<int>(pos % kPage) : 0;
+  const int s = kSlots ? 0 : s_seq;
+  const long long pos = kSlots ? place : s_pos;
+  const bool pos_ok = kSlots || (pos >= 0 && pos < static_cast<long long>(a.max_pages) * kPage);
+  const int lp = !kSlots && pos_ok ? static_cast<int>(pos / kPage) : 0;
+  const int slot = pos_ok ? static_cast<int>(pos % kPage) : 0;
+  using Page = std::conditional_t<kSlots, long long, int32_t>;
+  Page pid;
+  if constexpr (kSlots)
+    pid = place / kPage;
+  else
     pid = pos_ok ? a.block_table[static_cast<size_t>(s) * a.max_pages + lp] : -1;
-  }
 
   uint32_t code = 0;
   if (raw) {
