@@ -430,8 +430,8 @@ def kvtc_raw_cache_bytes(n_layers, n_pages, n_kv_heads):
 class RawCache:
     """Uncompressed page cache: pool [n_layers][n_pages][n_kv_heads][K, V][128][128] (bf16 or
     fp16), block table and status word (torch CUDA tensors), described to the library as a
-    kvtc_raw_cache.  An int32 block table on the device is used in place, so tables that
-    kvtc_step_tables grows are seen by later calls."""
+    kvtc_raw_cache.  A contiguous int32 block table on the device is used in place, so tables
+    that kvtc_step_tables grows are seen by later calls (any other is copied)."""
 
     def __init__(self, n_layers, n_kv_heads, n_pages, block_table, dtype=None, device="cuda", pool=None):
         import torch
